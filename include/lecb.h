@@ -524,6 +524,108 @@ int lecb_decode_fp32_from_results(const uint8_t* const d_stream[4], const lecb_r
                                   uint32_t* d_out, lecb_result* d_res4,
                                   void* d_ws, uint64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ operators of quantised layers
+ * What makes the 4-bit weights and 8-bit activations that the codec stores,
+ * and what a layer computes with them once they are decoded.
+ *
+ * Element types are the lecb_type below; strides count elements, rows of x,
+ * residual, weights and results may lie further apart than their length
+ * (stride >= row length), elements of a row are adjacent.  Results must not
+ * overlap inputs unless an entry says otherwise.  Unlike the codec's entries
+ * the tensors here need only the alignment of their element type (and their
+ * address and stride never change a result's bits); tiles, scales, workspaces
+ * and both sides of lecb_dequantize_q8 are 16-byte aligned.  Nothing here reports through a
+ * lecb_result: all errors are detected on the host.
+ *
+ * 4-bit weights W[n][k] are two's-complement codes q in -7..7 (codes from
+ * elsewhere may use -8) with one scale per row and `group` (32, 64 or 128)
+ * consecutive columns: w = q * s.  They are kept in tiles of 16 rows x 128
+ * columns, rows and columns padded with zero codes: eight codes of columns
+ * 8j .. 8j+7 make a 32-bit word (column 8j in bits 0-3; the same word as in
+ * the row-major form of two codes per byte), and
+ *   tiles  = u32 [ceil(n/16)][ceil(k/128)][4 c][16 r][4 d]: word (c, r, d) of a
+ *            tile holds row r, columns 32 d + 8 c .. +7 -- lane 16 c + r of a
+ *            wave reads its 16 bytes in one load, and word d of all lanes is
+ *            one matrix instruction's operand of 32 columns;
+ *   scales = type [ceil(n/16)][ceil(k/128) * 128/group][16 r], zero past n
+ *            and past the last group of k.
+ * The tiles are bytes like any other to the codec (lecb_encode: pairs of
+ * codes as symbols). */
+typedef enum { LECB_F32 = 0, LECB_BF16 = 1, LECB_F16 = 2, LECB_I8 = 3 } lecb_type;
+#define LECB_NORM_MAX_COLS 32768u
+
+/* Bytes of the tiles of W[n][k]; number of scales.  0 on bad arguments
+ * (n or k 0, group not 32, 64 or 128, n or k >= 2^31). */
+uint64_t lecb_w4_tile_bytes(uint64_t n, uint64_t k);
+uint64_t lecb_w4_scale_count(uint64_t n, uint64_t k, uint32_t group);
+
+/* Round W[n][k] (type F32, BF16 or F16, row stride w_stride) to 4-bit codes:
+ * s = max|w| / 7 over the group, rounded to 32 bits and then to scale_type
+ * (F32 or BF16); q = w / s rounded to the nearest whole number (the exact
+ * quotient decides, half a step goes to the even code), kept in -7..7; q = 0
+ * where s = 0.  A group that holds an infinity or NaN gets s = NaN and q = 0,
+ * so it reads back as NaN.  Errors: INVALID_ARG. */
+int lecb_quantize_w4(const void* d_w, int type, uint64_t w_stride, uint64_t n, uint64_t k,
+                     uint32_t group, uint8_t* d_tiles, void* d_scales, int scale_type, void* stream);
+
+/* out[n][k] = q * s, a product in 32 bits, rounded to `type` (F32, BF16 or
+ * F16), row stride out_stride.  Errors: INVALID_ARG. */
+int lecb_dequantize_w4(const uint8_t* d_tiles, const void* d_scales, int scale_type, uint32_t group,
+                       uint64_t n, uint64_t k, void* d_out, int type, uint64_t out_stride, void* stream);
+
+/* Row-major packed codes (ceil(k/2) bytes a row, column 2j in bits 0-3 of byte
+ * j, no padding between rows) into tiles, and back.  The unused half of a
+ * row's last byte (odd k) is ignored, and written as 0. */
+int lecb_tile_w4(const uint8_t* d_rows, uint64_t n, uint64_t k, uint8_t* d_tiles, void* stream);
+int lecb_untile_w4(const uint8_t* d_tiles, uint64_t n, uint64_t k, uint8_t* d_rows, void* stream);
+
+/* Residual addition, root-mean-square norm and quantisation to 8 bits, one
+ * pass: h = x + residual (d_res NULL: h = x), y_j = h_j * weight_j /
+ * sqrt(mean(h^2) + eps), scale = max|y| / 127, q = y / scale rounded to
+ * nearest in -127..127.  Sums in 32 bits, from the unrounded h.
+ *   x, residual, h: `type` (F32, BF16, F16); weight: weight_type, `cols` long;
+ *   d_h (may be NULL; may be d_x or d_res when its stride is the same): h
+ *   rounded to `type`; d_q: q, rows of `cols` bytes without padding;
+ *   d_scale: one float per row, written -- or, with static_scale = 1, ONE
+ *   float that is read and used for every row (a scale fixed beforehand, as
+ *   a fixed codebook is): q = y / scale saturates at -127 and 127.
+ * A row with an infinity or NaN, or whose sum of squares overflows 32 bits (some
+ * |h| above 2^63), gets scale = NaN and q = 0; a
+ * row of zeros gets scale 0 and q = 0.  With static_scale, NaN gives q = 0 and
+ * so does a scale that is not above 0.
+ * cols in 1..LECB_NORM_MAX_COLS, eps > 0 and finite.  rows 0 does nothing.
+ * Errors: INVALID_ARG, TOO_LARGE (rows >= 2^31). */
+int lecb_rmsnorm_q8(const void* d_x, uint64_t x_stride, const void* d_res, uint64_t res_stride,
+                    const void* d_weight, int weight_type, int type, uint64_t rows, uint32_t cols,
+                    float eps, void* d_h, uint64_t h_stride, int8_t* d_q, float* d_scale,
+                    int static_scale, void* stream);
+
+/* out[i][j] = q[i][j] * scale, a product in 32 bits, rounded to `type`; q and out rows of `cols`
+ * without padding, 16-byte aligned; scale_stride 1: one scale per row, 0: one scale.
+ * Errors: INVALID_ARG, TOO_LARGE (rows or cols >= 2^31, rows * cols >= 2^35). */
+int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const float* d_scale,
+                       int scale_stride, void* d_out, int type, void* stream);
+
+/* y[i][j] = sum_k x[i][k] * w[j][k] for m tokens against 4-bit weights W[n][k]:
+ * the sum over a group in 32 bits (whole numbers for x of I8), times the
+ * group's scale, added up in 32 bits; for x of I8 times d_xscale[i] (stride 1)
+ * or d_xscale[0] (stride 0); rounded once to y_type (F32, BF16, F16).
+ *   x: x_type I8, BF16 or F16, row stride x_stride; d_xscale: only for I8,
+ *   NULL = 1.
+ * The result does not depend on what else runs, and a token's row not on the
+ * other rows' values.  With x of BF16 or F16 a code enters the products as
+ * 24 + q and 24 sum(x) is taken off again (exact but for 32-bit rounding, at
+ * most 1/6 of whose bits it costs): entries of x above 2^120 or not finite
+ * make their token's row NaN or infinite.
+ * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken); its
+ * contents do not matter before or after.  m 0 does nothing.
+ * Errors: INVALID_ARG, WORKSPACE, TOO_LARGE (m >= 2^31). */
+uint64_t lecb_matvec_w4_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
+int lecb_matvec_w4(const void* d_x, int x_type, uint64_t x_stride, const float* d_xscale,
+                   int xscale_stride, uint64_t m, const uint8_t* d_tiles, const void* d_scales,
+                   int scale_type, uint32_t group, uint64_t n, uint64_t k, void* d_y, int y_type,
+                   uint64_t y_stride, void* d_ws, uint64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

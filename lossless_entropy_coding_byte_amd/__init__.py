@@ -6,6 +6,10 @@ one (torch tensors are passed by ``data_ptr()``, the stream is the current
 torch stream); the small helpers below them only allocate buffers with torch
 and chain those calls.  If the library is not built this module raises on
 first use -- there is no fallback of any kind.
+
+The operators of quantised layers (``quantize_w4``, ``rmsnorm_q8``,
+``matvec_w4`` and what goes with them) are defined in ``layers.py``, which
+needs torch, and are reached as attributes of this package.
 """
 
 from __future__ import annotations
@@ -137,7 +141,39 @@ _SIGNATURES = {
                                           _vp, _vp, _vp, _vp, _u64, _vp]),
     "lecb_decode_fp32": (_int, [_vp, _vp, _vp, _u32, _u64, _vp, _vp, _vp, _u64, _vp]),
     "lecb_decode_fp32_from_results": (_int, [_vp, _vp, _vp, _u32, _u64, _vp, _vp, _vp, _u64, _vp]),
+    "lecb_w4_tile_bytes": (_u64, [_u64, _u64]),
+    "lecb_w4_scale_count": (_u64, [_u64, _u64, _u32]),
+    "lecb_quantize_w4": (_int, [_vp, _int, _u64, _u64, _u64, _u32, _vp, _vp, _int, _vp]),
+    "lecb_dequantize_w4": (_int, [_vp, _vp, _int, _u32, _u64, _u64, _vp, _int, _u64, _vp]),
+    "lecb_tile_w4": (_int, [_vp, _u64, _u64, _vp, _vp]),
+    "lecb_untile_w4": (_int, [_vp, _u64, _u64, _vp, _vp]),
+    "lecb_rmsnorm_q8": (_int, [_vp, _u64, _vp, _u64, _vp, _int, _int, _u64, _u32, ctypes.c_float, _vp, _u64, _vp,
+                               _vp, _int, _vp]),
+    "lecb_dequantize_q8": (_int, [_vp, _u64, _u64, _vp, _int, _vp, _int, _vp]),
+    "lecb_matvec_w4_workspace_bytes": (_u64, [_u64, _u64, _u64]),
+    "lecb_matvec_w4": (_int, [_vp, _int, _u64, _vp, _int, _u64, _vp, _vp, _int, _u32, _u64, _u64, _vp, _int, _u64,
+                              _vp, _u64, _vp]),
 }
+
+# Names of layers.py that are this package's too (resolved on first use: importing
+# the codec's host functions alone does not import torch).
+_LAYERS = (
+    "W4Weights", "quantize_w4", "dequantize_w4", "tile_w4", "untile_w4", "rmsnorm_q8", "dequantize_q8", "matvec_w4",
+    "lecb_w4_tile_bytes", "lecb_w4_scale_count", "lecb_matvec_w4_workspace_bytes", "lecb_quantize_w4",
+    "lecb_dequantize_w4", "lecb_tile_w4", "lecb_untile_w4", "lecb_rmsnorm_q8", "lecb_dequantize_q8",
+    "lecb_matvec_w4", "LECB_F32", "LECB_BF16", "LECB_F16", "LECB_I8", "NORM_MAX_COLS",
+)
+
+
+def __getattr__(name):
+    if name not in _LAYERS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layers
+
+    for n in _LAYERS:
+        globals()[n] = getattr(layers, n)
+    return globals()[name]
+
 
 _lib = None
 

@@ -1,0 +1,447 @@
+// Rounding to 4 and 8 bits: quantize_w4 / dequantize_w4 / tile_w4 (weights in
+// tiles of 4-bit codes), rmsnorm_q8 / dequantize_q8 (activations in int8).
+// All of them move their data once and are bound by HBM; lecb.h states the
+// formulas and layouts.
+#include "layers.hpp"
+
+namespace lecb {
+
+namespace {
+
+constexpr uint32_t ABS_MASK = 0x7fffffffu;
+constexpr uint32_t INF_BITS = 0x7f800000u;
+
+// |v| as an unsigned number: orders like |v|, and any NaN above infinity, so
+// one unsigned maximum finds both the largest magnitude and what is not finite.
+__device__ inline uint32_t abs_bits(float v) { return __float_as_uint(v) & ABS_MASK; }
+__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// a * b rounded to 32 bits whatever is done with it next: the compiler would
+// fuse a product with its conversion to fp16, which rounds once where bf16 and
+// the formulas in lecb.h round twice.
+__device__ inline float product(float a, float b) {
+    float p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+
+// The step of a group and what turns weights into codes.  q = rint(w / s) of
+// the exact quotient: n = rint(w * (1/s)) is that or its neighbour (the
+// product is off by under two units in its last place), and e = w - n s is
+// exact (one fused operation, and both terms are multiples of the smaller
+// one's last place within 24 bits of s), so comparing |e| with s / 2 settles
+// it.  Steps below 2^-60 work on s and w times 2^64, so that neither 1/s nor
+// s / 2 leaves the range.
+struct Step {
+    float s;      // as stored (0: all codes 0; NaN: not finite)
+    float t;      // s * lift
+    float inv;    // 1 / t, or 0
+    float lift;   // 1 or 2^64
+    __device__ void set(uint32_t amax_bits, bool bf16) {
+        s = amax_bits >= INF_BITS ? __uint_as_float(0x7fc00000u) : __uint_as_float(amax_bits) / 7.0f;
+        if (bf16) s = (float)(__bf16)s;
+        // a step that rounding to 16 bits carried to infinity is none either
+        if (abs_bits(s) >= INF_BITS) s = __uint_as_float(0x7fc00000u);
+        lift = s < 0x1p-60f ? 0x1p64f : 1.0f;
+        t = s * lift;
+        inv = t > 0.0f ? 1.0f / t : 0.0f;
+    }
+    __device__ uint32_t code(float w) const {
+        const float v = w * lift;
+        float n = rintf(v * inv);
+        const float e = fmaf(-n, t, v), a = fabsf(e) + fabsf(e);
+        const bool odd = ((int)n & 1) != 0;
+        if (a > t || (a == t && odd)) n += e > 0.0f ? 1.0f : -1.0f;
+        n = fminf(fmaxf(n, -7.0f), 7.0f);
+        return inv > 0.0f ? (uint32_t)(int)n & 15u : 0u;
+    }
+};
+
+// One wave makes one tile: lane 16 c + r takes row r, columns 32 d + 8 c .. + 7
+// for d = 0..3 -- the four words of its 16 bytes -- so a group's maximum needs
+// the lanes r, r + 16, r + 32, r + 48 only, and the tile leaves in one store.
+template <typename T, int GROUP>
+__global__ __launch_bounds__(256) void quantize_w4_kernel(const T* __restrict__ w, uint64_t stride, uint64_t n,
+                                                          uint64_t k, uint32_t kt, uint32_t tiles,
+                                                          u32x4* __restrict__ out, void* __restrict__ scales,
+                                                          int bf16) {
+    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (tile >= tiles) return;
+    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint32_t tn = tile / kt, tk = tile % kt;
+    const uint64_t row = (uint64_t)tn * TILE_ROWS + r;
+    const uint64_t col = (uint64_t)tk * TILE_COLS + 8 * c;
+    Piece<T> v[4];
+    const uint64_t left = row < n && col < k ? k - col : 0;   // columns of this row from `col` on
+    const T* p = w + (left ? row * stride + col : 0);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d].load(p + 32 * d, left > 32u * d ? left - 32u * d : 0);
+    constexpr int WORDS = GROUP / 32, GROUPS = 4 / WORDS;
+    u32x4 words;
+    float mine = 0.0f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int d = g * WORDS; d < (g + 1) * WORDS; ++d)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = umax(a, abs_bits(v[d][i]));
+        a = umax(a, __shfl_xor(a, 16));
+        a = umax(a, __shfl_xor(a, 32));
+        Step st;
+        st.set(a, bf16);
+        if (c == (uint32_t)g) mine = st.s;
+#pragma unroll
+        for (int d = g * WORDS; d < (g + 1) * WORDS; ++d) {
+            uint32_t q = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q |= st.code(v[d][i]) << (4 * i);
+            words[d] = q;
+        }
+    }
+    out[(uint64_t)tile * 64 + lane] = words;
+    // lane 16 g + r holds the scale of group g, row r: the order they are stored in
+    if (c < (uint32_t)GROUPS) {
+        const uint64_t at = (uint64_t)tile * (GROUPS * 16) + lane;
+        if (bf16)
+            reinterpret_cast<__bf16*>(scales)[at] = (__bf16)mine;
+        else
+            reinterpret_cast<float*>(scales)[at] = mine;
+    }
+}
+
+__device__ inline float code_value(uint32_t word, int i) { return (float)((int)(word << (28 - 4 * i)) >> 28); }
+
+template <typename T>
+__global__ __launch_bounds__(256) void dequantize_w4_kernel(const u32x4* __restrict__ in,
+                                                            const void* __restrict__ scales, int bf16,
+                                                            uint32_t group, uint64_t n, uint64_t k, uint32_t kt,
+                                                            uint32_t tiles, T* __restrict__ out, uint64_t stride) {
+    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (tile >= tiles) return;
+    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint64_t row = (uint64_t)(tile / kt) * TILE_ROWS + r;
+    const uint64_t col = (uint64_t)(tile % kt) * TILE_COLS + 8 * c;
+    const u32x4 words = in[(uint64_t)tile * 64 + lane];
+    if (row >= n || col >= k) return;
+    T* p = out + row * stride + col;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint64_t at = ((uint64_t)tile * (TILE_COLS / group) + 32 * d / group) * 16 + r;
+        const float s = bf16 ? (float)reinterpret_cast<const __bf16*>(scales)[at]
+                             : reinterpret_cast<const float*>(scales)[at];
+        Piece<T> v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.set(i, product(code_value(words[d], i), s));
+        if (col + 32 * d < k) v.store(p + 32 * d, k - col - 32 * d);
+    }
+}
+
+// Row-major codes <-> tiles: both hold the same 32-bit words, in another order.
+// A row's last word may be partial: it goes by bytes, without the unused half.
+__global__ __launch_bounds__(256) void tile_w4_kernel(const uint8_t* __restrict__ rows, u32x4* __restrict__ out,
+                                                      uint64_t n, uint64_t k, uint32_t kt, uint32_t tiles) {
+    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (tile >= tiles) return;
+    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint64_t row = (uint64_t)(tile / kt) * TILE_ROWS + r;
+    const uint64_t col = (uint64_t)(tile % kt) * TILE_COLS + 8 * c;
+    const uint64_t pitch = (k + 1) / 2;
+    u32x4 words = {0, 0, 0, 0};
+    if (row < n) {
+        const uint8_t* p = rows + row * pitch;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint64_t c0 = col + 32 * d;
+            if (c0 + 8 <= k) {
+                words[d] = *reinterpret_cast<const u32_loose*>(p + c0 / 2);
+            } else {
+                for (uint32_t i = 0; i < 8 && c0 + i < k; ++i)
+                    words[d] |= ((uint32_t)p[(c0 + i) / 2] >> (4 * (i & 1)) & 15u) << (4 * i);
+            }
+        }
+    }
+    out[(uint64_t)tile * 64 + lane] = words;
+}
+
+__global__ __launch_bounds__(256) void untile_w4_kernel(const u32x4* __restrict__ in, uint8_t* __restrict__ rows,
+                                                        uint64_t n, uint64_t k, uint32_t kt, uint32_t tiles) {
+    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (tile >= tiles) return;
+    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint64_t row = (uint64_t)(tile / kt) * TILE_ROWS + r;
+    const uint64_t col = (uint64_t)(tile % kt) * TILE_COLS + 8 * c;
+    const uint64_t pitch = (k + 1) / 2;
+    if (row >= n) return;
+    const u32x4 words = in[(uint64_t)tile * 64 + lane];
+    uint8_t* p = rows + row * pitch;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint64_t c0 = col + 32 * d;
+        if (c0 + 8 <= k) {
+            *reinterpret_cast<u32_loose*>(p + c0 / 2) = words[d];
+        } else {
+            for (uint32_t i = 0; i < 8 && c0 + i < k; i += 2) {
+                const uint32_t v = words[d] >> (4 * i) & 255u;
+                p[(c0 + i) / 2] = (uint8_t)(c0 + i + 1 < k ? v : v & 15u);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- 8-bit activations
+
+// One workgroup of THREADS lanes per row, the row in registers (NV pieces of
+// eight elements a lane).  With a = max|h weight|, the scale is a r / 127 for
+// r = 1 / sqrt(mean(h^2) + eps) and the codes are rint(h weight 127 / a): r
+// cancels, so the sum of squares and the maximum come out of one pass and one
+// reduction.
+template <int THREADS>
+struct RowSums {
+    float ss;
+    uint32_t amax;
+    __device__ void reduce() {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            ss += __shfl_xor(ss, o);
+            amax = umax(amax, __shfl_xor(amax, o));
+        }
+        if (THREADS > 64) {
+            constexpr int W = THREADS / 64;
+            __shared__ float s_ss[W];
+            __shared__ uint32_t s_max[W];
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) {
+                s_ss[threadIdx.x >> 6] = ss;
+                s_max[threadIdx.x >> 6] = amax;
+            }
+            __syncthreads();
+            ss = s_ss[0];
+            amax = s_max[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                ss += s_ss[i];
+                amax = umax(amax, s_max[i]);
+            }
+        }
+    }
+};
+
+struct NormArgs {
+    const void* x;
+    const void* res;
+    const void* weight;
+    void* h;
+    int8_t* q;
+    float* scale;
+    uint64_t x_stride, res_stride, h_stride;
+    uint32_t rows, cols;
+    float eps;
+    int static_scale;
+};
+
+template <typename T, typename W, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) void rmsnorm_q8_kernel(NormArgs a) {
+    const uint64_t row = blockIdx.x;
+    const uint32_t cols = a.cols, c0 = threadIdx.x * 8;
+    const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
+    const T* res = a.res ? reinterpret_cast<const T*>(a.res) + row * a.res_stride : nullptr;
+    T* h = a.h ? reinterpret_cast<T*>(a.h) + row * a.h_stride : nullptr;
+    const W* weight = reinterpret_cast<const W*>(a.weight);
+    int8_t* q = a.q + row * cols;
+    float v[NV][8];
+    RowSums<THREADS> sums{0.0f, 0u};
+#pragma unroll
+    for (int p = 0; p < NV; ++p) {
+        const uint32_t c = c0 + p * THREADS * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+        if (c < cols) {
+            Piece<T> b;
+            b.load(x + c, cols - c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[p][i] = b[i];
+            if (res) {
+                b.load(res + c, cols - c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[p][i] += b[i];
+            }
+            if (h) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b.set(i, v[p][i]);
+                b.store(h + c, cols - c);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums.ss = fmaf(v[p][i], v[p][i], sums.ss);
+            Piece<W> w;
+            w.load(weight + c, cols - c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[p][i] *= w[i];   // from here on v = h weight
+                sums.amax = umax(sums.amax, abs_bits(v[p][i]));
+            }
+        }
+    }
+    sums.reduce();
+    const float r = 1.0f / sqrtf(sums.ss / (float)cols + a.eps);
+    float mul;           // codes are rint(v * lift * mul)
+    float lift = 1.0f;
+    bool none = false;   // no code but 0
+    if (a.static_scale) {
+        const float s = a.scale[0];
+        none = !(s > 0.0f);
+        mul = r / s;
+    } else {
+        const float amax = __uint_as_float(sums.amax);
+        const bool bad = sums.amax >= INF_BITS || abs_bits(sums.ss) >= INF_BITS;
+        const float s = bad ? __uint_as_float(0x7fc00000u) : amax * r / 127.0f;
+        none = bad || !(s > 0.0f);
+        if (amax < 0x1p-60f) lift = 0x1p64f;   // 127 / amax stays in range
+        mul = 127.0f / (amax * lift);
+        if (threadIdx.x == 0) a.scale[row] = s;
+    }
+#pragma unroll
+    for (int p = 0; p < NV; ++p) {
+        const uint32_t c = c0 + p * THREADS * 8;
+        if (c >= cols) continue;
+        u32x2 b = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = v[p][i] * lift * mul;
+            const int code = none || !(y == y) ? 0 : (int)rintf(fminf(fmaxf(y, -127.0f), 127.0f));
+            b[i / 4] |= ((uint32_t)code & 255u) << (8 * (i % 4));
+        }
+        if (cols - c >= 8) {
+            *reinterpret_cast<u32x2_loose*>(q + c) = b;
+        } else {
+            for (uint32_t i = 0; i < cols - c; ++i) q[c + i] = (int8_t)(b[i / 4] >> (8 * (i % 4)));
+        }
+    }
+}
+
+// A lane turns 16 neighbouring codes into values; a piece may span rows.
+template <typename T>
+__global__ __launch_bounds__(256) void dequantize_q8_kernel(const int8_t* __restrict__ q, uint64_t total,
+                                                            uint32_t cols, const float* __restrict__ scale,
+                                                            int scale_stride, T* __restrict__ out) {
+    const uint64_t at = ((uint64_t)blockIdx.x * 256 + threadIdx.x) * 16;
+    if (at >= total) return;
+    uint64_t row = scale_stride ? at / cols : 0;
+    uint32_t col = scale_stride ? (uint32_t)(at - row * cols) : 0;
+    float s = scale[row];
+    const bool whole = at + 16 <= total;
+    u32x4 b = {0, 0, 0, 0};
+    if (whole) {
+        b = *reinterpret_cast<const u32x4*>(q + at);
+    } else {
+        for (uint32_t i = 0; at + i < total; ++i) b[i / 4] |= (uint32_t)(uint8_t)q[at + i] << (8 * (i % 4));
+    }
+    Piece<T> v[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i / 8].set(i % 8, product((float)((int)(b[i / 4] << (24 - 8 * (i % 4))) >> 24), s));
+        if (scale_stride && ++col == cols && at + i + 1 < total) {
+            col = 0;
+            s = scale[++row];
+        }
+    }
+    v[0].store(out + at, total - at);
+    if (total - at > 8) v[1].store(out + at + 8, total - at - 8);
+}
+
+template <typename T, typename W>
+int launch_norm_as(const NormArgs& a, hipStream_t s) {
+    const dim3 grid(a.rows);
+    const uint32_t pieces = (a.cols + 7) / 8;
+    if (pieces <= 64)
+        rmsnorm_q8_kernel<T, W, 64, 1><<<grid, 64, 0, s>>>(a);
+    else if (pieces <= 256)
+        rmsnorm_q8_kernel<T, W, 256, 1><<<grid, 256, 0, s>>>(a);
+    else if (pieces <= 1024)
+        rmsnorm_q8_kernel<T, W, 256, 4><<<grid, 256, 0, s>>>(a);
+    else
+        rmsnorm_q8_kernel<T, W, 1024, 4><<<grid, 1024, 0, s>>>(a);
+    return launched();
+}
+
+}  // namespace
+
+int launch_quantize_w4(const QuantizeW4& a, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const uint64_t kt = tiles_of(a.k, TILE_COLS), tiles = tiles_of(a.n, TILE_ROWS) * kt;
+    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
+    const dim3 grid((uint32_t)((tiles + 3) / 4));
+    const int bf16 = a.scale_type == LECB_BF16;
+    return with_float_type(a.type, [&](auto t) -> int {
+        typedef decltype(t) T;
+        auto go = [&](auto group) {
+            constexpr int G = decltype(group)::value;
+            quantize_w4_kernel<T, G><<<grid, 256, 0, s>>>(static_cast<const T*>(a.w), a.stride, a.n, a.k, (uint32_t)kt, (uint32_t)tiles,
+                                        reinterpret_cast<u32x4*>(a.tiles), a.scales, bf16);
+        };
+        if (a.group == 32)
+            go(std::integral_constant<int, 32>());
+        else if (a.group == 64)
+            go(std::integral_constant<int, 64>());
+        else
+            go(std::integral_constant<int, 128>());
+        return launched();
+    });
+}
+
+int launch_dequantize_w4(const DequantizeW4& a, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const uint64_t kt = tiles_of(a.k, TILE_COLS), tiles = tiles_of(a.n, TILE_ROWS) * kt;
+    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
+    const dim3 grid((uint32_t)((tiles + 3) / 4));
+    return with_float_type(a.type, [&](auto t) -> int {
+        typedef decltype(t) T;
+        dequantize_w4_kernel<T><<<grid, 256, 0, s>>>(reinterpret_cast<const u32x4*>(a.tiles), a.scales, a.scale_type == LECB_BF16,
+                                    a.group, a.n, a.k, (uint32_t)kt, (uint32_t)tiles, static_cast<T*>(a.out),
+                                    a.stride);
+        return launched();
+    });
+}
+
+int launch_tile_w4(const uint8_t* rows, uint8_t* tiles_out, uint64_t n, uint64_t k, void* stream) {
+    const uint64_t kt = tiles_of(k, TILE_COLS), tiles = tiles_of(n, TILE_ROWS) * kt;
+    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
+    tile_w4_kernel<<<dim3((uint32_t)((tiles + 3) / 4)), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+        rows, reinterpret_cast<u32x4*>(tiles_out), n, k, (uint32_t)kt, (uint32_t)tiles);
+    return launched();
+}
+
+int launch_untile_w4(const uint8_t* tiles_in, uint8_t* rows, uint64_t n, uint64_t k, void* stream) {
+    const uint64_t kt = tiles_of(k, TILE_COLS), tiles = tiles_of(n, TILE_ROWS) * kt;
+    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
+    untile_w4_kernel<<<dim3((uint32_t)((tiles + 3) / 4)), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+        reinterpret_cast<const u32x4*>(tiles_in), rows, n, k, (uint32_t)kt, (uint32_t)tiles);
+    return launched();
+}
+
+int launch_rmsnorm_q8(const RmsnormQ8& a, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const NormArgs b = {a.x, a.res, a.weight, a.h, a.q, a.scale, a.x_stride, a.res_stride, a.h_stride,
+                        (uint32_t)a.rows, a.cols, a.eps, a.static_scale};
+    return with_float_type(a.type, [&](auto t) -> int {
+        return with_float_type(a.weight_type, [&](auto w) -> int {
+            return launch_norm_as<decltype(t), decltype(w)>(b, s);
+        });
+    });
+}
+
+int launch_dequantize_q8(const int8_t* q, uint64_t rows, uint64_t cols, const float* scale, int scale_stride,
+                         void* out, int type, void* stream) {
+    const uint64_t total = rows * cols;
+    const dim3 grid((uint32_t)((total + 4095) / 4096));
+    return with_float_type(type, [&](auto t) -> int {
+        typedef decltype(t) T;
+        dequantize_q8_kernel<T><<<grid, 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+            q, total, (uint32_t)cols, scale, scale_stride, static_cast<T*>(out));
+        return launched();
+    });
+}
+
+}  // namespace lecb

@@ -1,0 +1,264 @@
+"""Operators of quantised layers on torch tensors: what makes the 4-bit weights
+and 8-bit activations that the codec stores, and what a layer computes with them.
+
+``lecb_*`` functions mirror the C ABI of ``include/lecb.h`` (explicit buffers,
+optional stream); the functions below them check shapes, types and devices
+(``ValueError``), allocate their results with torch and run on the current
+stream of the current device.  Every step runs in the HIP library.
+
+>>> w4 = quantize_w4(weight)                             # [n, k] float -> 4-bit tiles + scales
+>>> q, scale, h = rmsnorm_q8(x, norm_weight, residual=r) # h = x + r; q int8, scale per row
+>>> y = matvec_w4(q, w4, x_scale=scale)                  # [rows, n] bf16
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import LecbError, _check, _ptr, _stream, load  # noqa: F401
+
+LECB_F32, LECB_BF16, LECB_F16, LECB_I8 = 0, 1, 2, 3
+NORM_MAX_COLS = 32768
+
+_TYPES = {torch.float32: LECB_F32, torch.bfloat16: LECB_BF16, torch.float16: LECB_F16, torch.int8: LECB_I8}
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_SCALES = (torch.float32, torch.bfloat16)
+
+
+def _type(dtype, allowed, what):
+    if dtype not in allowed:
+        raise ValueError(f"{what}: {dtype} is not one of {', '.join(str(d) for d in allowed)}")
+    return _TYPES[dtype]
+
+
+# --------------------------------------------------------------------------- the C ABI, one to one
+
+def lecb_w4_tile_bytes(n: int, k: int) -> int:
+    return load().lecb_w4_tile_bytes(n, k)
+
+
+def lecb_w4_scale_count(n: int, k: int, group: int) -> int:
+    return load().lecb_w4_scale_count(n, k, group)
+
+
+def lecb_matvec_w4_workspace_bytes(m: int, n: int, k: int) -> int:
+    return load().lecb_matvec_w4_workspace_bytes(m, n, k)
+
+
+def lecb_quantize_w4(w, w_stride, n, k, group, tiles, scales, stream=None) -> None:
+    _check(load().lecb_quantize_w4(_ptr(w), _TYPES[w.dtype], w_stride, n, k, group, _ptr(tiles), _ptr(scales),
+                                   _TYPES[scales.dtype], _stream(stream)), "lecb_quantize_w4")
+
+
+def lecb_dequantize_w4(tiles, scales, group, n, k, out, out_stride, stream=None) -> None:
+    _check(load().lecb_dequantize_w4(_ptr(tiles), _ptr(scales), _TYPES[scales.dtype], group, n, k, _ptr(out),
+                                     _TYPES[out.dtype], out_stride, _stream(stream)), "lecb_dequantize_w4")
+
+
+def lecb_tile_w4(rows, n, k, tiles, stream=None) -> None:
+    _check(load().lecb_tile_w4(_ptr(rows), n, k, _ptr(tiles), _stream(stream)), "lecb_tile_w4")
+
+
+def lecb_untile_w4(tiles, n, k, rows, stream=None) -> None:
+    _check(load().lecb_untile_w4(_ptr(tiles), n, k, _ptr(rows), _stream(stream)), "lecb_untile_w4")
+
+
+def lecb_rmsnorm_q8(x, x_stride, res, res_stride, weight, rows, cols, eps, h, h_stride, q, scale,
+                    static_scale: bool = False, stream=None) -> None:
+    _check(load().lecb_rmsnorm_q8(_ptr(x), x_stride, _ptr(res), res_stride, _ptr(weight), _TYPES[weight.dtype],
+                                  _TYPES[x.dtype], rows, cols, eps, _ptr(h), h_stride, _ptr(q), _ptr(scale),
+                                  int(static_scale), _stream(stream)), "lecb_rmsnorm_q8")
+
+
+def lecb_dequantize_q8(q, rows, cols, scale, scale_stride, out, stream=None) -> None:
+    _check(load().lecb_dequantize_q8(_ptr(q), rows, cols, _ptr(scale), scale_stride, _ptr(out),
+                                     _TYPES[out.dtype], _stream(stream)), "lecb_dequantize_q8")
+
+
+def lecb_matvec_w4(x, x_stride, x_scale, x_scale_stride, m, tiles, scales, group, n, k, y, y_stride, ws=None,
+                   stream=None) -> None:
+    _check(load().lecb_matvec_w4(_ptr(x), _TYPES[x.dtype], x_stride, _ptr(x_scale), x_scale_stride, m, _ptr(tiles),
+                                 _ptr(scales), _TYPES[scales.dtype], group, n, k, _ptr(y), _TYPES[y.dtype], y_stride,
+                                 _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
+                                 _stream(stream)), "lecb_matvec_w4")
+
+
+# --------------------------------------------------------------------------- tensors
+
+def _here(*tensors):
+    """Checks that every tensor is on the current device."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+            raise ValueError(f"tensor on {t.device}: the current GPU's memory is needed")
+
+
+def _rows_of(x, what):
+    """x as (rows, cols, row stride): any leading dimensions that are one stride apart, adjacent columns."""
+    if x.dim() == 0:
+        raise ValueError(f"{what}: at least one dimension is needed")
+    cols = x.shape[-1]
+    if x.is_contiguous():
+        return (x.numel() // cols if cols else 0), cols, cols
+    if cols > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    rows = 1
+    stride = None
+    for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * rows:
+            raise ValueError(f"{what}: rows must be one stride apart (strides {tuple(x.stride())})")
+        rows *= size
+    stride = cols if stride is None else stride
+    if stride < cols:
+        raise ValueError(f"{what}: rows overlap (strides {tuple(x.stride())})")
+    return rows, cols, stride
+
+
+class W4Weights:
+    """4-bit weights [n, k] in the tile order of ``include/lecb.h``: ``tiles``
+    (uint8, lecb_w4_tile_bytes) and ``scales`` (float32 or bfloat16,
+    lecb_w4_scale_count; shape [ceil(n/16), groups, 16])."""
+
+    __slots__ = ("tiles", "scales", "n", "k", "group")
+
+    def __init__(self, tiles, scales, n: int, k: int, group: int = 128):
+        if n < 1 or k < 1 or group not in (32, 64, 128):
+            raise ValueError("W4Weights: n and k are at least 1, group is 32, 64 or 128")
+        cells = -(-n // 16) * -(-k // 128)
+        if tiles.dtype != torch.uint8 or tiles.numel() != cells * 1024 or not tiles.is_contiguous():
+            raise ValueError(f"W4Weights: tiles are {cells * 1024} contiguous uint8")
+        _type(scales.dtype, _SCALES, "scales")
+        if scales.numel() != cells * (2048 // group) or not scales.is_contiguous():
+            raise ValueError(f"W4Weights: scales are {cells * (2048 // group)} contiguous numbers")
+        self.tiles, self.scales, self.n, self.k, self.group = tiles, scales, n, k, group
+
+
+def quantize_w4(w, group: int = 128, scale_dtype=torch.bfloat16) -> W4Weights:
+    """Round a float matrix [n, k] to 4-bit codes with one scale per row and ``group`` columns."""
+    if w.dim() != 2 or 0 in w.shape:
+        raise ValueError("quantize_w4: a matrix [n, k] is needed")
+    _type(w.dtype, _FLOATS, "quantize_w4")
+    _type(scale_dtype, _SCALES, "scale_dtype")
+    if group not in (32, 64, 128):
+        raise ValueError("quantize_w4: group is 32, 64 or 128")
+    n, k, stride = _rows_of(w, "quantize_w4")
+    _here(w)
+    nt, kt = -(-n // 16), -(-k // 128)
+    tiles = torch.empty((nt, kt, 1024), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((nt, kt * (128 // group), 16), dtype=scale_dtype, device=w.device)
+    lecb_quantize_w4(w, stride, n, k, group, tiles, scales)
+    return W4Weights(tiles, scales, n, k, group)
+
+
+def dequantize_w4(w4: W4Weights, dtype=torch.bfloat16):
+    """The weights [n, k] that the codes stand for."""
+    _type(dtype, _FLOATS, "dequantize_w4")
+    _here(w4.tiles, w4.scales)
+    out = torch.empty((w4.n, w4.k), dtype=dtype, device=w4.tiles.device)
+    lecb_dequantize_w4(w4.tiles, w4.scales, w4.group, w4.n, w4.k, out, w4.k)
+    return out
+
+
+def tile_w4(rows, n: int, k: int):
+    """Row-major codes (uint8 [n, ceil(k/2)], column 2j in the low half of byte j) as tiles."""
+    if rows.dtype != torch.uint8 or n < 1 or k < 1 or rows.numel() != n * ((k + 1) // 2) or not rows.is_contiguous():
+        raise ValueError("tile_w4: n * ceil(k / 2) contiguous uint8 are needed")
+    _here(rows)
+    tiles = torch.empty((-(-n // 16), -(-k // 128), 1024), dtype=torch.uint8, device=rows.device)
+    lecb_tile_w4(rows, n, k, tiles)
+    return tiles
+
+
+def untile_w4(tiles, n: int, k: int):
+    """Tiles back to row-major codes, uint8 [n, ceil(k/2)]."""
+    if (tiles.dtype != torch.uint8 or n < 1 or k < 1 or not tiles.is_contiguous()
+            or tiles.numel() != -(-n // 16) * -(-k // 128) * 1024):
+        raise ValueError("untile_w4: the contiguous uint8 tiles of [n, k] are needed")
+    _here(tiles)
+    rows = torch.empty((n, (k + 1) // 2), dtype=torch.uint8, device=tiles.device)
+    lecb_untile_w4(tiles, n, k, rows)
+    return rows
+
+
+def rmsnorm_q8(x, weight, residual=None, eps: float = 1e-6, scale=None, out_h=None):
+    """h = x + residual, its root-mean-square norm times weight, in 8 bits.
+
+    x, residual [..., cols] of one float type; weight [cols].  Returns (q int8
+    [..., cols], scale float32 [...], h in x's type).  Without a residual h is
+    x itself.  scale: a float32 tensor of one number fixes the scale for every
+    row (values past it saturate) and is returned as given.  out_h: where h
+    goes; x or residual themselves will do."""
+    rows, cols, xs = _rows_of(x, "rmsnorm_q8")
+    _type(x.dtype, _FLOATS, "rmsnorm_q8")
+    _type(weight.dtype, _FLOATS, "rmsnorm_q8: weight")
+    if not 1 <= cols <= NORM_MAX_COLS:
+        raise ValueError(f"rmsnorm_q8: rows have 1 to {NORM_MAX_COLS} columns")
+    if weight.numel() != cols or not weight.is_contiguous():
+        raise ValueError("rmsnorm_q8: weight holds one contiguous number per column")
+    _here(x, weight, residual, scale, out_h)
+    rs, h, hs = 0, None, 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("rmsnorm_q8: residual has x's shape and type")
+        _, _, rs = _rows_of(residual, "rmsnorm_q8: residual")
+        h = out_h if out_h is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if h.shape != x.shape or h.dtype != x.dtype:
+            raise ValueError("rmsnorm_q8: out_h has x's shape and type")
+        _, _, hs = _rows_of(h, "rmsnorm_q8: out_h")
+    elif out_h is not None:
+        raise ValueError("rmsnorm_q8: without a residual h is x")
+    if scale is None:
+        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        s = scale
+        if s.dtype != torch.float32 or s.numel() != 1:
+            raise ValueError("rmsnorm_q8: a fixed scale is one float32 number")
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    lecb_rmsnorm_q8(x, xs, residual, rs, weight, rows, cols, eps, h, hs, q, s, scale is not None)
+    return q, s, (x if h is None else h)
+
+
+def dequantize_q8(q, scale, dtype=torch.bfloat16):
+    """The values q * scale of int8 codes [..., cols]; scale: one float32 per row, or one."""
+    _type(dtype, _FLOATS, "dequantize_q8")
+    if q.dtype != torch.int8 or not q.is_contiguous() or q.dim() == 0:
+        raise ValueError("dequantize_q8: contiguous int8 codes are needed")
+    cols = q.shape[-1]
+    rows = q.numel() // cols if cols else 0
+    if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() not in (1, rows):
+        raise ValueError("dequantize_q8: one float32 scale per row, or one")
+    _here(q, scale)
+    out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    lecb_dequantize_q8(q, rows, cols, scale, int(scale.numel() != 1), out)
+    return out
+
+
+def matvec_w4(x, w4: W4Weights, x_scale=None, out_dtype=None, ws=None):
+    """y = x W^T for tokens x [..., k] of int8 (x_scale: float32, one per row or one), bfloat16 or float16.
+
+    Returns y [..., n] of out_dtype (x's type; bfloat16 for int8 x).  ws: a
+    uint8 workspace of lecb_matvec_w4_workspace_bytes that the caller keeps;
+    calls that overlap in time must not share one."""
+    m, k, xs = _rows_of(x, "matvec_w4")
+    if k != w4.k:
+        raise ValueError(f"matvec_w4: x has {k} columns, the weights {w4.k}")
+    is_int = x.dtype == torch.int8
+    if not is_int:
+        _type(x.dtype, (torch.int8, torch.bfloat16, torch.float16), "matvec_w4")
+    step = 0
+    if x_scale is not None:
+        if not is_int or x_scale.dtype != torch.float32 or not x_scale.is_contiguous() or x_scale.numel() not in (1, m):
+            raise ValueError("matvec_w4: x_scale goes with int8 x, one float32 per row or one")
+        step = int(x_scale.numel() != 1)
+    dtype = out_dtype if out_dtype is not None else torch.bfloat16 if is_int else x.dtype
+    _type(dtype, _FLOATS, "matvec_w4: out_dtype")
+    _here(x, w4.tiles, w4.scales, x_scale, ws)
+    y = torch.empty((*x.shape[:-1], w4.n), dtype=dtype, device=x.device)
+    if ws is None:
+        need = lecb_matvec_w4_workspace_bytes(m, w4.n, w4.k)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    lecb_matvec_w4(x, xs, x_scale, step, m, w4.tiles, w4.scales, w4.group, w4.n, w4.k, y, w4.n, ws)
+    return y
