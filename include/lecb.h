@@ -613,10 +613,7 @@ int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const fl
  *   x: x_type I8, BF16 or F16, row stride x_stride; d_xscale: only for I8,
  *   NULL = 1.
  * The result does not depend on what else runs, and a token's row not on the
- * other rows' values.  With x of BF16 or F16 a code enters the products as
- * 24 + q and 24 sum(x) is taken off again (exact but for 32-bit rounding, at
- * most 1/6 of whose bits it costs): entries of x above 2^120 or not finite
- * make their token's row NaN or infinite.
+ * other rows' values.
  * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken); its
  * contents do not matter before or after.  m 0 does nothing.
  * Errors: INVALID_ARG, WORKSPACE, TOO_LARGE (m >= 2^31). */

@@ -87,6 +87,7 @@ struct MatvecW4 {
     uint64_t y_stride;
     void* ws;
 };
+int device_cu_count();   // lecb_internal.hpp
 uint64_t matvec_w4_workspace(uint64_t m, uint64_t n, uint64_t k);
 int launch_matvec_w4(const MatvecW4& a, void* stream);
 
