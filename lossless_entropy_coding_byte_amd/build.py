@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "liblecb.so")
 ARCH = "gfx950"
 
 SOURCES = ["kernels_misc.hip", "kernels_codebook.hip", "kernels_encode.hip", "kernels_decode.hip", "codebook.cpp",
-           "host.cpp", "api.cpp", "noalloc.hip", "kernels_quant.hip", "kernels_matvec.hip", "api_layers.cpp"]
+           "host.cpp", "api.cpp", "noalloc.hip", "kernels_quant.hip", "kernels_matvec.hip", "kernels_matmul.hip",
+           "api_layers.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
