@@ -13,6 +13,14 @@ namespace lecb {
 
 namespace {
 
+// Waits for this wave's LDS accesses and then for the other waves.  Loads from
+// memory stay in flight: only the lanes that asked for them read what they bring.
+__device__ inline void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 constexpr int MM_WAVES = 8;
 constexpr int MM_TOKENS = 64;
 constexpr int MM_ROWS = 64;   // of W, a wave's
@@ -97,29 +105,39 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
 
     u32x4 words[4], next_words[4], next_x[P];
     S scale[4][GROUPS];
+    // A step's loads are in flight while the step before it is computed; the
+    // columns that do not fill a tile are guarded loads and come with commit.
     auto fetch = [&](uint32_t tk) {
+        if (tk < whole) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const uint32_t unit = (p * (64 * WN) + share) % T::UNITS;
-            const X* at = row[p] + (uint64_t)tk * TILE_COLS;
-            next_x[p] = tk < whole ? T::load(at, unit) : T::load(at, unit, rest);
+            for (int p = 0; p < P; ++p)
+                next_x[p] = T::load(row[p] + (uint64_t)tk * TILE_COLS, (p * (64 * WN) + share) % T::UNITS);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            next_words[j] = (tiles[j] + (uint64_t)tk * 64)[lane];
-        }
+        for (int j = 0; j < 4; ++j) next_words[j] = (tiles[j] + (uint64_t)tk * 64)[lane];
     };
     auto commit = [&](uint32_t tk, uint32_t buffer) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const uint32_t u = p * (64 * WN) + share;
-            sh.x[buffer][wk][T::place(u / T::UNITS, u % T::UNITS)] = next_x[p];
-        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             words[j] = next_words[j];
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) scale[j][g] = (scales[j] + ((uint64_t)tk * GROUPS + g) * 16)[r];
+        }
+        u32x4* x = sh.x[buffer][wk];
+        if (tk < whole) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const uint32_t u = p * (64 * WN) + share;
+                x[T::place(u / T::UNITS, u % T::UNITS)] = next_x[p];
+            }
+        } else {
+#pragma unroll 1
+            for (uint32_t u = share; u < UNITS; u += 64 * WN) {
+                const uint64_t t = m0 + u / T::UNITS;
+                x[T::place(u / T::UNITS, u % T::UNITS)] =
+                    T::load(reinterpret_cast<const X*>(a.x) + (t < a.m ? t : a.m - 1) * a.x_stride +
+                                (uint64_t)tk * TILE_COLS, u % T::UNITS, rest);
+            }
         }
     };
 
@@ -190,7 +208,7 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
     }
     for (uint32_t s = 0; s < steps; ++s) {
         const uint32_t tk = s * WK + wk;
-        __syncthreads();   // this tile is there, and the last one is read
+        lds_barrier();   // this tile is there, and the last one is read
         if (tk + WK < a.kt) fetch(tk + WK);
         if (tk < a.kt) compute(s & 1);
         if (tk + WK < a.kt) commit(tk + WK, (s + 1) & 1);
@@ -198,7 +216,7 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
 
     // The columns' shares are added up in a fixed order, and a lane stores four
     // neighbouring outputs.
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -206,7 +224,7 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 sh.y[wk][16 * i + 4 * c + e][wn * MM_ROWS + 16 * j + r] = sum[i][j][e];
-    __syncthreads();
+    lds_barrier();
     for (uint32_t at = threadIdx.x; at < MM_TOKENS * COLS / 4; at += 64 * MM_WAVES) {
         const uint32_t t = at / (COLS / 4), col = at % (COLS / 4) * 4;
         const uint64_t token = m0 + t, out = (uint64_t)n0 * 16 + col;
