@@ -9,72 +9,74 @@ namespace lecb {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// A word's eight codes as the matrix instruction's operand, eight entries of x
-// as the other, and their product.
+// Operands of the matrix instructions for tokens of type X, and their product.
 //
-// 16-bit x: the codes become q / 16, exactly: one conversion each (the even
-// codes from the word, the odd ones from the word shifted by four, byte by
-// byte) and one packing per pair.  int8 x: a code's four bits as the upper
-// half of a byte, 16 q, even columns and odd columns in a register each; x is
-// put into the same order.  FACTOR takes the sixteen off again, exactly.
+// An instruction takes 32 columns (64 for bytes in pairs of words): of a token
+// (first operand) and of a row of W (second), eight of them from each lane in
+// any order that both sides share.
+//
+// bytes: a code's four bits as the upper half of a byte, 16 q, the even
+// columns and the odd ones in a register each.
+//
+// 16 bits: a code's four bits, the sign's turned over, as the upper bits of the
+// mantissa of 2^-8: 2^-8 (1 + (q + 8) / 16), exactly, for one logic operation a
+// pair of codes (columns p and p + 4) after one shift; a conversion to float
+// and a packing take four times as long.  What is too much, 1.5 2^-8 times the
+// group's sum of x, is put into the sum beforehand: by an instruction whose
+// second operand is EXCESS, or from sums made before (Tokens).  2^-8 keeps the
+// sum over a group within the range of x.  FACTOR undoes 16 and 2^-8.
 template <typename X>
 struct Operand;
 
-__device__ inline void code_floats(uint32_t w, float* f) {   // f[i] = code i / 16
-    uint32_t u = w >> 4;
-    asm("" : "+v"(u));   // keeps one shift, so that every other conversion picks its byte itself
-    f[0] = __builtin_amdgcn_cvt_off_f32_i4(w);
-    f[1] = __builtin_amdgcn_cvt_off_f32_i4(u);
-    f[2] = __builtin_amdgcn_cvt_off_f32_i4((w >> 8) & 255u);
-    f[3] = __builtin_amdgcn_cvt_off_f32_i4((u >> 8) & 255u);
-    f[4] = __builtin_amdgcn_cvt_off_f32_i4(w >> 16);
-    f[5] = __builtin_amdgcn_cvt_off_f32_i4(u >> 16);
-    f[6] = __builtin_amdgcn_cvt_off_f32_i4(w >> 24);
-    f[7] = __builtin_amdgcn_cvt_off_f32_i4(u >> 24);
+// Pairs of halves (p, p + 4), p = 0..3, out of eight halves in order.
+__device__ inline u32x4 pairs_of_halves(u32x4 x) {
+    return {__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
+            __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
 }
 
 template <>
 struct Operand<__bf16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float FACTOR = 16.0f;
+    static constexpr float FACTOR = 4096.0f;
+    static constexpr bool OFFSET = true;
+    static constexpr uint32_t EXCESS = 0xBBC0BBC0u;   // -1.5 2^-8, twice
     static __device__ A weights(uint32_t w) {
-        float f[8];
-        code_floats(w, f);
-        A a;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            a[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)f[2 * i], (__bf16)f[2 * i + 1]});
-        return a;
+        return {((w << 3) & 0x00780078u) ^ 0x3BC03BC0u, ((w >> 1) & 0x00780078u) ^ 0x3BC03BC0u,
+                ((w >> 5) & 0x00780078u) ^ 0x3BC03BC0u, ((w >> 9) & 0x00780078u) ^ 0x3BC03BC0u};
     }
-    static __device__ A tokens(A x) { return x; }
+    static __device__ u32x4 order(u32x4 x) { return pairs_of_halves(x); }
     static __device__ Acc mul(A a, A b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
+    }
+    static __device__ float dot(uint32_t a, uint32_t b, float c) {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
     }
 };
 template <>
 struct Operand<_Float16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float FACTOR = 16.0f;
+    static constexpr float FACTOR = 4096.0f;
+    static constexpr bool OFFSET = true;
+    static constexpr uint32_t EXCESS = 0x9E009E00u;
     static __device__ A weights(uint32_t w) {
-        float f[8];
-        code_floats(w, f);
-        A a;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            a[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f[2 * i], f[2 * i + 1]));
-        return a;
+        return {((w << 6) & 0x03C003C0u) ^ 0x1E001E00u, ((w << 2) & 0x03C003C0u) ^ 0x1E001E00u,
+                ((w >> 2) & 0x03C003C0u) ^ 0x1E001E00u, ((w >> 6) & 0x03C003C0u) ^ 0x1E001E00u};
     }
-    static __device__ A tokens(A x) { return x; }
+    static __device__ u32x4 order(u32x4 x) { return pairs_of_halves(x); }
     static __device__ Acc mul(A a, A b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                       0, 0, 0);
+    }
+    static __device__ float dot(uint32_t a, uint32_t b, float c) {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
     }
 };
 template <>
@@ -82,81 +84,57 @@ struct Operand<int8_t> {
     typedef u32x2 A;
     typedef i32x4 Acc;
     static constexpr float FACTOR = 0.0625f;
+    static constexpr bool OFFSET = false;
     static __device__ A weights(uint32_t w) { return {(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u}; }
-    static __device__ A tokens(A x) {
-        return {__builtin_amdgcn_perm(x.y, x.x, 0x06040200u), __builtin_amdgcn_perm(x.y, x.x, 0x07050301u)};
+    // two times eight bytes
+    static __device__ u32x4 order(u32x4 x) {
+        return {__builtin_amdgcn_perm(x.y, x.x, 0x06040200u), __builtin_amdgcn_perm(x.y, x.x, 0x07050301u),
+                __builtin_amdgcn_perm(x.w, x.z, 0x06040200u), __builtin_amdgcn_perm(x.w, x.z, 0x07050301u)};
     }
     static __device__ Acc mul(A a, A b, Acc c) {
         return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0,
                                                      0, 0);
     }
     // two words at once: 64 columns an instruction, at twice the rate
-    static __device__ Acc mul2(A a0, A a1, A b0, A b1, Acc c) {
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{(int)a0.x, (int)a0.y, (int)a1.x, (int)a1.y},
+    static __device__ Acc mul2(u32x4 a, A b0, A b1, Acc c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
                                                      i32x4{(int)b0.x, (int)b0.y, (int)b1.x, (int)b1.y}, c, 0, 0, 0);
     }
 };
 
-// Eight entries of a row of x; the guarded form takes `count` of them (zeros
-// past that) and is used where a row's last tile is partial.
+// A token's 128 columns of a tile as 16-byte units, each what a lane gives one
+// instruction of 16 bits or of 64 columns of bytes: 16 bits, unit u holds
+// columns 8 u ..; bytes, unit 4 p + c holds columns 64 p + 8 c .. and 64 p + 32
+// + 8 c ...  So lane 16 c + r takes units 4 p + c of token r, p < PIECES.
 template <typename X>
-__device__ inline typename Operand<X>::A load_x8(const X* p) {
-    typedef typename Operand<X>::A A;
-    typedef A loose __attribute__((aligned(sizeof(X))));
-    return *reinterpret_cast<const loose*>(p);
-}
-template <typename X>
-__device__ inline typename Operand<X>::A load_x8(const X* p, uint64_t count) {
-    if (count >= 8) return load_x8(p);
-    typename Operand<X>::A v{};
-    constexpr int PER = 4 / sizeof(X), BITS = 8 * sizeof(X);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if ((uint64_t)i >= count) continue;
-        const uint32_t e = sizeof(X) == 1 ? reinterpret_cast<const uint8_t*>(p)[i]
-                                          : reinterpret_cast<const uint16_t*>(p)[i];
-        v[i / PER] |= e << (BITS * (i % PER));
-    }
-    return v;
-}
-
-// Four neighbouring scales as loaded, and as numbers.
-template <typename S>
-struct Scales {
-    typedef S raw __attribute__((ext_vector_type(4)));
-    raw v;
-    __device__ void load(const S* p) { v = *reinterpret_cast<const raw*>(p); }
-    __device__ float operator[](int i) const { return (float)v[i]; }
-};
-
-// The last step of a sum: the token's factor, one rounding, four outputs.
-__device__ inline void store_y(void* y, int type, uint64_t at, uint64_t left, f32x4 v) {
-    if (left >= 4) {
-        if (type == LECB_F32) {
-            typedef f32x4 loose __attribute__((aligned(4)));
-            *reinterpret_cast<loose*>(reinterpret_cast<float*>(y) + at) = v;
-        } else if (type == LECB_BF16) {
-            typedef bf16x4 loose __attribute__((aligned(2)));
-            *reinterpret_cast<loose*>(reinterpret_cast<__bf16*>(y) + at) =
-                bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+struct Tokens {
+    static constexpr int PIECES = 2 * sizeof(X), UNITS = 4 * PIECES;
+    typedef u32x2 u32x2_any __attribute__((aligned(1)));
+    typedef u32x4 u32x4_any __attribute__((aligned(1)));
+    static __device__ u32x4 load(const X* tile, uint32_t unit) {
+        if constexpr (sizeof(X) == 1) {
+            const X* p = tile + 64 * (unit >> 2) + 8 * (unit & 3);
+            const u32x2 a = *reinterpret_cast<const u32x2_any*>(p), b = *reinterpret_cast<const u32x2_any*>(p + 32);
+            return {a.x, a.y, b.x, b.y};
         } else {
-            typedef f16x4 loose __attribute__((aligned(2)));
-            *reinterpret_cast<loose*>(reinterpret_cast<_Float16*>(y) + at) =
-                f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+            return *reinterpret_cast<const u32x4_any*>(tile + 8 * unit);
         }
-        return;
     }
+    // the tile's first `left` columns only, zeros after them
+    static __device__ u32x4 load(const X* tile, uint32_t unit, uint32_t left) {
+        constexpr int N = 16 / sizeof(X), PER = 4 / sizeof(X), BITS = 8 * sizeof(X);
+        u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if ((uint64_t)e >= left) continue;
-        if (type == LECB_F32)
-            reinterpret_cast<float*>(y)[at + e] = v[e];
-        else if (type == LECB_BF16)
-            reinterpret_cast<__bf16*>(y)[at + e] = (__bf16)v[e];
-        else
-            reinterpret_cast<_Float16*>(y)[at + e] = (_Float16)v[e];
+        for (int i = 0; i < N; ++i) {
+            const uint32_t c = sizeof(X) == 1 ? 64 * (unit >> 2) + 8 * (unit & 3) + 32 * (i / 8) + i % 8 : 8 * unit + i;
+            if (c >= left) continue;
+            const uint32_t e = sizeof(X) == 1 ? reinterpret_cast<const uint8_t*>(tile)[c]
+                                              : reinterpret_cast<const uint16_t*>(tile)[c];
+            v[i / PER] |= e << (BITS * (i % PER));
+        }
+        return v;
     }
-}
+};
 
 struct MatvecArgs {
     const void* x;
@@ -164,11 +142,85 @@ struct MatvecArgs {
     const u32x4* tiles;
     const void* scales;
     void* y;
+    void* ws;
     uint64_t x_stride, y_stride, n, k, m;
     uint32_t nt, kt;
     int xscale_stride, y_type;
 };
 
+// The last step of a sum: the token's factor, one rounding, four outputs.
+__device__ inline void store_y(const MatvecArgs& a, uint64_t token, uint64_t col, f32x4 v) {
+    const uint64_t at = token * a.y_stride + col, left = a.n - col;
+    if (a.xscale) v *= a.xscale[a.xscale_stride ? token : 0];
+    if (left >= 4) {
+        if (a.y_type == LECB_F32) {
+            typedef f32x4 loose __attribute__((aligned(4)));
+            *reinterpret_cast<loose*>(reinterpret_cast<float*>(a.y) + at) = v;
+        } else if (a.y_type == LECB_BF16) {
+            typedef bf16x4 loose __attribute__((aligned(2)));
+            *reinterpret_cast<loose*>(reinterpret_cast<__bf16*>(a.y) + at) =
+                bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        } else {
+            typedef f16x4 loose __attribute__((aligned(2)));
+            *reinterpret_cast<loose*>(reinterpret_cast<_Float16*>(a.y) + at) =
+                f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        if ((uint64_t)e >= left) continue;
+        if (a.y_type == LECB_F32)
+            reinterpret_cast<float*>(a.y)[at + e] = v[e];
+        else if (a.y_type == LECB_BF16)
+            reinterpret_cast<__bf16*>(a.y)[at + e] = (__bf16)v[e];
+        else
+            reinterpret_cast<_Float16*>(a.y)[at + e] = (_Float16)v[e];
+    }
+}
+
+// Waits for this wave's LDS accesses and then for the other waves.  Loads from
+// memory to registers stay in flight.
+__device__ inline void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// BYTES (4 or 16) from each lane's address straight to LDS, lane after lane
+// from `to` on (the same in every lane); there after loads_done and, for the
+// other waves, a barrier.
+template <int BYTES>
+__device__ inline void load_to_lds(const void* from, void* to) {
+    typedef const __attribute__((address_space(1))) void* Global;
+    typedef __attribute__((address_space(3))) void* Lds;
+    if constexpr (BYTES == 16)   // the builtin takes no dependent size
+        __builtin_amdgcn_global_load_lds((Global)from, (Lds)to, 16, 0, 0);
+    else
+        __builtin_amdgcn_global_load_lds((Global)from, (Lds)to, 4, 0, 0);
+}
+__device__ inline void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Tokens laid out for the products, in the workspace: 16-byte units, ordered,
+// [16 tokens][kt][PIECES][64 lanes] -- a piece of 1 KiB is one load of a wave --
+// and for 16 bits -1.5 2^-8 times each group's sum of each token, [64 tokens]
+// [kt][4][groups][16 tokens].  Tokens past m and columns past k are zeros.
+constexpr int LAID_TOKENS = 64;   // the workspace holds a multiple of these
+__host__ __device__ inline uint64_t laid_units(uint64_t m, uint64_t kt, uint64_t bytes) {
+    return (m + LAID_TOKENS - 1) / LAID_TOKENS * LAID_TOKENS * kt * (8 * bytes);
+}
+inline uint64_t laid_bytes(uint64_t m, uint64_t kt) {   // of the widest type, with sums of the smallest groups
+    return laid_units(m, kt, 2) * 16 + (m + LAID_TOKENS - 1) / LAID_TOKENS * LAID_TOKENS * kt * (4 * 4);
+}
+inline __device__ const u32x4* laid_tokens(const MatvecArgs& a) { return reinterpret_cast<const u32x4*>(a.ws); }
+template <typename X>
+__device__ inline float* laid_sums(const MatvecArgs& a) {
+    return reinterpret_cast<float*>(reinterpret_cast<u32x4*>(a.ws) + laid_units(a.m, a.kt, sizeof(X)));
+}
+
+constexpr uint64_t FEW_IN_ROWS = 8;   // tokens that are read from their rows
+
+int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, uint64_t blocks, hipStream_t s);   // of 16 tokens
 int launch_matmul_w4(const MatvecArgs& a, int x_type, int scale_type, uint32_t group, hipStream_t s);
 
 }  // namespace lecb
