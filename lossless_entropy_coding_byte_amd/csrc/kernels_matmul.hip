@@ -17,13 +17,14 @@ __device__ inline float add_lanes(float v) {   // v + the v of the lane that CTR
 // A workgroup takes 16 tokens and the columns of 256 units: one tile of 16-bit
 // tokens, two of bytes.  Lanes read along the tokens' rows and write along the
 // pieces, through LDS (the XOR spreads both over the banks).
-template <typename X>
+template <typename X, bool MANY>
 __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t group, uint32_t across) {
     typedef Operand<X> O;
     typedef Tokens<X> T;
     constexpr int TILES = 16 / T::UNITS;
     __shared__ u32x4 sh[256];
-    const uint32_t mt = blockIdx.x / across, tk0 = blockIdx.x % across * TILES, unit = threadIdx.x % T::UNITS, sub = threadIdx.x / T::UNITS % TILES;
+    const uint32_t mt = blockIdx.x / across, tk0 = blockIdx.x % across * TILES;
+    const uint32_t unit = threadIdx.x % T::UNITS, sub = threadIdx.x / T::UNITS % TILES;
     const uint32_t token = threadIdx.x / 16, tk = tk0 + sub;
     const uint64_t t = (uint64_t)mt * 16 + token, col = (uint64_t)tk * TILE_COLS;
     u32x4 v = {0, 0, 0, 0};
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t 
         const X* p = reinterpret_cast<const X*>(a.x) + t * a.x_stride + col;
         v = O::order(col + TILE_COLS <= a.k ? T::load(p, unit) : T::load(p, unit, (uint32_t)(a.k - col)));
     }
-    if constexpr (O::OFFSET) {
+    if constexpr (O::OFFSET && MANY) {
         // 16 neighbouring lanes hold a token's tile, group / 8 of them a group
         float s = 0.0f;
 #pragma unroll
@@ -42,14 +43,18 @@ __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t 
         if (group >= 128) s = add_lanes<0x140>(s);  // mirrored within sixteen
         const uint32_t per = group / 8, groups = 16 / per;
         if (tk < a.kt && unit % per == 0)
-            laid_sums<X>(a)[((((uint64_t)(mt / 4) * a.kt + tk) * 4 + mt % 4) * groups + unit / per) * 16 + token] = s;
+            laid_sums<X>(a)[(((uint64_t)(mt / 4) * a.kt + tk) * groups + unit / per) * 64 + mt % 4 * 16 + token] = s;
     }
     sh[(sub * T::UNITS + unit) * 16 + (token ^ unit)] = v;
     __syncthreads();
     const uint32_t u = threadIdx.x / 16, r = threadIdx.x % 16;   // unit of TILES tiles, token
-    if (tk0 + u / T::UNITS < a.kt)
-        reinterpret_cast<u32x4*>(a.ws)[((uint64_t)mt * a.kt + tk0) * (16 * T::UNITS) + threadIdx.x] =
-            sh[u * 16 + (r ^ (u % T::UNITS))];
+    const uint32_t tk1 = tk0 + u / T::UNITS, u1 = u % T::UNITS;
+    if (tk1 >= a.kt) return;
+    // MANY: piece 2 p + s, lane 32 h + (mt odd: 16) + r, for unit 4 p + 2 h + s
+    const uint64_t at = MANY ? ((uint64_t)(mt / 2) * a.kt + tk1) * (32 * T::UNITS) + (u1 / 4 * 2 + u1 % 2) * 64 +
+                                   u1 / 2 % 2 * 32 + mt % 2 * 16 + r
+                             : ((uint64_t)mt * a.kt + tk1) * (16 * T::UNITS) + u1 * 16 + r;
+    reinterpret_cast<u32x4*>(a.ws)[at] = sh[u * 16 + (r ^ u1)];
 }
 
 // ---------------------------------------------------------------- products
@@ -57,35 +62,39 @@ __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t 
 constexpr int MM_WAVES = 8;
 constexpr int MM_ROWS = 64;   // of W, a wave's
 
-// A workgroup takes 64 tokens and 64 WN rows of W; its eight waves are WN along
-// the rows times 8 / WN along the columns.  A wave keeps 64 x 64 sums in
-// registers: its words of W come from memory as the matrix instructions take
-// them, become numbers there and serve four instructions each; the tokens come
-// through LDS, where the WN waves of one share of the columns put each tile
-// once, by loads that go there directly.
-template <typename X, int GROUP>
-struct MmTile {   // 64 tokens' tile
-    u32x4 x[4 * Tokens<X>::PIECES][64];
-    float excess[Operand<X>::OFFSET ? 64 * (128 / GROUP) : 4];   // [4][groups][16 tokens]
+// What a share of the columns has in LDS of one tile of 128 columns: 64 tokens
+// and 64 WN rows of W.
+template <typename X, typename S, int GROUP, int WN>
+struct MmTile {
+    static constexpr int GROUPS = 128 / GROUP, PIECES = 2 * Tokens<X>::PIECES;
+    static constexpr int SCALES = GROUPS * 4 * 16, LOADS = SCALES * sizeof(S) < 256 ? 1 : SCALES * sizeof(S) / 256;
+    u32x4 x[2 * PIECES][64];
+    u32x4 words[WN][4][64];
+    S scales[WN][LOADS * 256 / sizeof(S)];                // [4][groups][16 rows]
+    float excess[Operand<X>::OFFSET ? GROUPS : 1][64];    // of each token
 };
 
 // Sends for one tile while the other is computed.  The compiler keeps the reads
 // of `now` apart from the loads on their way to `next` for being told here that
 // the two are different memory: it would wait for those loads first otherwise.
-template <typename Tile, typename Fetch, typename Compute>
-__device__ __forceinline__ void mm_step(const Tile* __restrict__ now, Tile* __restrict__ next, Fetch fetch, Compute compute) {
-    fetch(next);
-    compute(now);
+template <typename Tile, typename F>
+__device__ __forceinline__ void mm_step(const Tile* __restrict__ now, Tile* __restrict__ next, F f) {
+    f(now, next);
 }
 
+// A workgroup takes 64 tokens and 64 WN rows of W; its eight waves are WN along
+// the rows times 8 / WN along the columns.  A wave keeps 64 x 64 sums in
+// registers.  Everything comes through LDS, by loads that go there directly and
+// are sent one tile ahead: a share's tokens once for its WN waves, each wave's
+// own words and scales.  Products go by 32 tokens x 32 rows: beside matrix
+// instructions a SIMD sends one vector instruction in about 4.5 cycles, so their
+// number is what counts, and these take half as many as 16 x 16 ones.
 template <typename X, typename S, int GROUP, int WN>
 __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, uint32_t mblocks, uint32_t blocks) {
     typedef Operand<X> O;
-    typedef Tokens<X> T;
-    constexpr int WK = MM_WAVES / WN, GROUPS = 128 / GROUP, WORDS = GROUP / 32;
-    constexpr int PIECES = 4 * T::PIECES;                  // of 64 tokens' tile
-    constexpr int COLS = MM_ROWS * WN, PITCH = COLS + 4;   // outputs of a token; + 4: rows on other banks
-    typedef MmTile<X, GROUP> Tile;
+    typedef MmTile<X, S, GROUP, WN> Tile;
+    constexpr int WK = MM_WAVES / WN, GROUPS = 128 / GROUP, WORDS = GROUP / 32, PIECES = Tile::PIECES;
+    constexpr int COLS = MM_ROWS * WN, PITCH = COLS + 8;   // outputs of a token; + 8: rows on other banks
     union Shared {
         Tile tile[2][WK];
         float y[WK][LAID_TOKENS][PITCH];
@@ -99,142 +108,146 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
     if ((blockIdx.x >> 3) >= per || id >= blocks) return;
     const uint32_t mb = id % mblocks, n0 = id / mblocks * (COLS / 16);   // 64 tokens, tile of W
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, wk = wave / WN;
-    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint32_t lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
 
-    const u32x4* tiles[4];
-    const S* scales[4];
+    // tiles past the last repeat it: their sums are not stored
+    auto tile_row = [&](uint32_t j) -> uint64_t { return n0 + wn * 4 + j < a.nt ? n0 + wn * 4 + j : a.nt - 1; };
+    const u32x4* from_words[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // tiles past the last repeat it: their sums are not stored
-        const uint64_t t = n0 + wn * 4 + j, tn = t < a.nt ? t : a.nt - 1;
-        tiles[j] = a.tiles + tn * a.kt * 64;
-        scales[j] = reinterpret_cast<const S*>(a.scales) + tn * a.kt * (GROUPS * 16);
+    for (int j = 0; j < 4; ++j) from_words[j] = a.tiles + tile_row(j) * a.kt * 64;
+    const char* from_scales[Tile::LOADS];   // four bytes of the four tiles' scales
+    constexpr uint32_t ROW = GROUPS * 16 * sizeof(S);
+#pragma unroll
+    for (int q = 0; q < Tile::LOADS; ++q) {
+        const uint32_t b = (q * 256 + lane * 4) % (4 * ROW);
+        from_scales[q] = reinterpret_cast<const char*>(a.scales) + tile_row(b / ROW) * a.kt * ROW + b % ROW;
     }
-    const u32x4* x = laid_tokens(a) + (uint64_t)mb * a.kt * (PIECES * 64);
-    const float* excess = laid_sums<X>(a) + (uint64_t)mb * a.kt * (64 * GROUPS);
+    const u32x4* from_x = laid_tokens(a) + (uint64_t)mb * a.kt * (2 * PIECES * 64);
+    const float* from_excess = laid_sums<X>(a) + (uint64_t)mb * a.kt * (GROUPS * 64);
 
-    u32x4 words[4], next_words[4];
-    S scale[4][GROUPS], next_scale[4][GROUPS];
-    auto fetch = [&](uint32_t tk, Tile* tile) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = 0; q < PIECES / WN; ++q) {
-            const uint32_t p = q * WN + wn;
-            // piece p of the four blocks of 16 tokens, which lie a.kt tiles apart
-            const u32x4* from = x + ((uint64_t)(p / T::PIECES) * a.kt + tk) * (T::PIECES * 64) + p % T::PIECES * 64;
-            load_to_lds<16>(from + lane, tile->x[p]);
-        }
-        if constexpr (O::OFFSET) {
-            if (wn == 0) {
-#pragma unroll
-                for (int g = 0; g < GROUPS; ++g)
-                    load_to_lds<4>(excess + ((uint64_t)tk * GROUPS + g) * 64 + lane, tile->excess + 64 * g);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            next_words[j] = (tiles[j] + (uint64_t)tk * 64)[lane];
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) next_scale[j][g] = (scales[j] + ((uint64_t)tk * GROUPS + g) * 16)[r];
+    constexpr int SENDS = 2 * PIECES / WN + 4 + Tile::LOADS + (O::OFFSET ? 1 : 0);
+    auto send = [&](uint32_t tk, Tile* tile, int i) __attribute__((always_inline)) {
+        constexpr int A = 2 * PIECES / WN, B = A + 4, C = B + Tile::LOADS;
+        if (i < A) {
+            // piece p of the two blocks of 32 tokens, which lie a.kt tiles apart
+            const uint32_t p = i * WN + wn;
+            load_to_lds<16>(from_x + ((uint64_t)(p / PIECES) * a.kt + tk) * (PIECES * 64) + p % PIECES * 64 + lane, tile->x[p]);
+        } else if (i < B) {
+            load_to_lds<16>(from_words[i - A] + (uint64_t)tk * 64 + lane, tile->words[wn][i - A]);
+        } else if (i < C) {
+            load_to_lds<4>(from_scales[i - B] + (uint64_t)tk * ROW, &tile->scales[wn][(i - B) * (256 / sizeof(S))]);
+        } else {   // by several waves alike
+            load_to_lds<4>(from_excess + ((uint64_t)tk * GROUPS + wn % GROUPS) * 64 + lane, tile->excess[wn % GROUPS]);
         }
     };
 
-    f32x4 sum[4][4];
+    f32x16 sum[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] = {0, 0, 0, 0};
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[i][j][e] = 0.0f;
 
-    auto compute = [&](const Tile* tile) __attribute__((always_inline)) {
+    // A group's columns, then 32 rows of W: those words become numbers and the
+    // rows before are scaled while the matrix instructions run.
+    auto step = [&](uint32_t tk, const Tile* now, Tile* next) __attribute__((always_inline)) {
+        const uint32_t ahead = tk + WK < a.kt ? tk + WK : a.kt - 1;   // past the last: sent again, not used
+        typedef decltype(O::mul32({}, {}, {})) Acc;
+        constexpr int N = sizeof(X) == 2 ? 2 * WORDS : WORDS == 1 ? 2 : WORDS;   // pieces of a group
+        constexpr int UNITS = 2 * GROUPS;
+        u32x4 words[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) words[j][s] = now->words[wn][2 * j + r / 16][(2 * h + s) * 16 + r % 16];
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            typename O::Acc acc[4][4];
-            if constexpr (sizeof(X) == 1 && WORDS > 1) {
+            u32x4 xo[2][N];
 #pragma unroll
-                for (int d = 0; d < WORDS; d += 2) {
-                    u32x4 xo[4];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xo[i] = tile->x[i * T::PIECES + (g * WORDS + d) / 2][lane];
+                for (int p = 0; p < N; ++p)
+                    xo[i][p] = now->x[i * PIECES + (sizeof(X) == 1 && WORDS == 1 ? g / 2 * 2 : g * N) + p][lane];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u32x2 w0 = O::weights(words[j][g * WORDS + d]), w1 = O::weights(words[j][g * WORDS + d + 1]);
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[i][j] = O::mul2(xo[i], w0, w1, d ? acc[i][j] : typename O::Acc{0, 0, 0, 0});
+                for (int q = 0; q < SENDS; ++q)   // spread over the units
+                    if (q * UNITS / SENDS == g * 2 + j) send(ahead, next, q);
+                Acc acc[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (O::OFFSET) {   // token 32 i + 8 q + 4 h + e
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(&now->excess[g][32 * i + 8 * q + 4 * h]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][4 * q + e] = v[e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[i][e] = 0;
                     }
                 }
-            } else if constexpr (sizeof(X) == 1) {
-                u32x2 xo[4];   // half a unit
+                if constexpr (sizeof(X) == 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x4 v = tile->x[i * T::PIECES + g / 2][lane];
-                    xo[i] = g & 1 ? u32x2{v.z, v.w} : u32x2{v.x, v.y};
-                }
+                    for (int p = 0; p < N; ++p) {
+                        const u32x4 w = O::weights(words[j][p % 2][g * WORDS + p / 2]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x2 w = O::weights(words[j][g]);
+                        for (int i = 0; i < 2; ++i) acc[i] = O::mul32(xo[i][p], w, acc[i]);
+                    }
+                } else if constexpr (WORDS == 1) {   // half a unit
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i][j] = O::mul(xo[i], w, typename O::Acc{0, 0, 0, 0});
-                }
-            } else {
-                f32x4 over[4];
+                    for (int p = 0; p < 2; ++p) {
+                        const u32x2 w = O::weights(words[j][p][g]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    over[i] = *reinterpret_cast<const f32x4*>(&tile->excess[(i * GROUPS + g) * 16 + 4 * c]);
+                        for (int i = 0; i < 2; ++i)
+                            acc[i] = O::mul32(g & 1 ? u32x2{xo[i][p].z, xo[i][p].w} : u32x2{xo[i][p].x, xo[i][p].y}, w, acc[i]);
+                    }
+                } else {
 #pragma unroll
-                for (int d = 0; d < WORDS; ++d) {
-                    u32x4 xo[4];
+                    for (int p = 0; p < N; ++p) {
+                        const u32x2 w0 = O::weights(words[j][p % 2][g * WORDS + p / 2 * 2]);
+                        const u32x2 w1 = O::weights(words[j][p % 2][g * WORDS + p / 2 * 2 + 1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xo[i] = tile->x[i * T::PIECES + g * WORDS + d][lane];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u32x4 w = O::weights(words[j][g * WORDS + d]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[i][j] = O::mul(xo[i], w, d ? acc[i][j] : over[i]);
+                        for (int i = 0; i < 2; ++i) acc[i] = O::mul32x2(xo[i][p], w0, w1, acc[i]);
                     }
                 }
+                const float s = (float)now->scales[wn][((2 * j + r / 16) * GROUPS + g) * 16 + r % 16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[i][j][e] = fmaf((float)acc[i][e], s, sum[i][j][e]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s = (float)scale[j][g];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[i][j][e] = fmaf((float)acc[i][j][e], s, sum[i][j][e]);
-            }
-            // four groups a tile: moving one's loads and words into another runs out of registers
-            if (GROUPS == 4) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    // Every wave takes the same number of steps; those past the last tile only
-    // wait.  A step's loads are in flight while the step before is computed.
+    // Every wave takes the same number of steps; those past the last tile only wait.
     const uint32_t steps = (a.kt + WK - 1) / WK;
-    if (wk < a.kt) fetch(wk, &sh.tile[0][wk]);
+    if (wk < a.kt) {
+#pragma unroll
+        for (int q = 0; q < SENDS; ++q) send(wk, &sh.tile[0][wk], q);
+    }
     for (uint32_t s = 0; s < steps; ++s) {
         const uint32_t tk = s * WK + wk;
         loads_done();
         lds_barrier();   // this tile is there, and the last one is read
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            words[j] = next_words[j];
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) scale[j][g] = next_scale[j][g];
-        }
-        mm_step<Tile>(
-            &sh.tile[s & 1][wk], &sh.tile[(s + 1) & 1][wk],
-            [&](Tile* tile) __attribute__((always_inline)) { if (tk + WK < a.kt) fetch(tk + WK, tile); },
-            [&](const Tile* tile) __attribute__((always_inline)) { if (tk < a.kt) compute(tile); });
+        if (tk < a.kt)
+            mm_step<Tile>(&sh.tile[s & 1][wk], &sh.tile[(s + 1) & 1][wk],
+                          [&](const Tile* now, Tile* next) __attribute__((always_inline)) { step(tk, now, next); });
     }
 
     // The columns' shares are added up in a fixed order, and a lane stores four
     // neighbouring outputs.
+    loads_done();
     lds_barrier();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sh.y[wk][16 * i + 4 * c + e][wn * MM_ROWS + 16 * j + r] = sum[i][j][e];
+            for (int e = 0; e < 16; ++e)
+                sh.y[wk][32 * i + e / 4 * 8 + 4 * h + e % 4][wn * MM_ROWS + 32 * j + r] = sum[i][j][e];
     lds_barrier();
     for (uint32_t at = threadIdx.x; at < LAID_TOKENS * COLS / 4; at += 64 * MM_WAVES) {
         const uint32_t t = at / (COLS / 4), col = at % (COLS / 4) * 4;
@@ -278,20 +291,24 @@ int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s
 }
 
 template <typename X>
-int lay_as(const MatvecArgs& a, uint32_t group, uint64_t blocks, hipStream_t s) {
+int lay_as(const MatvecArgs& a, uint32_t group, bool many, hipStream_t s) {
     const uint64_t across = tiles_of(a.kt, 16 / Tokens<X>::UNITS);
-    if (blocks * across >= 1u << 31) return LECB_ERR_TOO_LARGE;
-    lay_tokens_kernel<X><<<dim3((uint32_t)(blocks * across)), 256, 0, s>>>(a, group, (uint32_t)across);
+    const uint64_t blocks = across * (many ? tiles_of(a.m, LAID_TOKENS) * (LAID_TOKENS / 16) : tiles_of(a.m, 16));
+    if (blocks >= 1u << 31) return LECB_ERR_TOO_LARGE;
+    if (many)
+        lay_tokens_kernel<X, true><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, group, (uint32_t)across);
+    else
+        lay_tokens_kernel<X, false><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, group, (uint32_t)across);
     return launched();
 }
 
 }  // namespace
 
-int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, uint64_t blocks, hipStream_t s) {
+int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s) {
     switch (x_type) {
-        case LECB_I8: return lay_as<int8_t>(a, group, blocks, s);
-        case LECB_BF16: return lay_as<__bf16>(a, group, blocks, s);
-        default: return lay_as<_Float16>(a, group, blocks, s);
+        case LECB_I8: return lay_as<int8_t>(a, group, many, s);
+        case LECB_BF16: return lay_as<__bf16>(a, group, many, s);
+        default: return lay_as<_Float16>(a, group, many, s);
     }
 }
 

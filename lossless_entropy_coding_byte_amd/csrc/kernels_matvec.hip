@@ -277,8 +277,7 @@ int launch_matvec_w4(const MatvecW4& m, void* stream) {
                        m.y_stride, m.n, m.k, m.m, (uint32_t)tiles_of(m.n, TILE_ROWS), (uint32_t)tiles_of(m.k, TILE_COLS),
                        m.xscale_stride, m.y_type};
     if (a.m > FEW_IN_ROWS) {
-        const uint64_t blocks = many(a) ? tiles_of(a.m, LAID_TOKENS) * (LAID_TOKENS / 16) : tiles_of(a.m, 16);
-        const int rc = launch_lay_tokens(a, m.x_type, m.group, blocks, s);
+        const int rc = launch_lay_tokens(a, m.x_type, m.group, many(a), s);
         if (rc) return rc;
         if (many(a)) return launch_matmul_w4(a, m.x_type, m.scale_type, m.group, s);
     }

@@ -13,6 +13,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Operands of the matrix instructions for tokens of type X, and their product.
 //
@@ -55,6 +57,10 @@ struct Operand<__bf16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
     }
+    static __device__ f32x16 mul32(u32x4 a, u32x4 b, f32x16 c) {   // 32 tokens, 32 rows, 16 columns
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
     static __device__ float dot(uint32_t a, uint32_t b, float c) {
         return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
     }
@@ -74,6 +80,10 @@ struct Operand<_Float16> {
     static __device__ Acc mul(A a, A b, Acc c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                       0, 0, 0);
+    }
+    static __device__ f32x16 mul32(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
     }
     static __device__ float dot(uint32_t a, uint32_t b, float c) {
         return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
@@ -98,6 +108,14 @@ struct Operand<int8_t> {
     // two words at once: 64 columns an instruction, at twice the rate
     static __device__ Acc mul2(u32x4 a, A b0, A b1, Acc c) {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                     i32x4{(int)b0.x, (int)b0.y, (int)b1.x, (int)b1.y}, c, 0, 0, 0);
+    }
+    static __device__ i32x16 mul32(A a, A b, i32x16 c) {
+        return __builtin_amdgcn_mfma_i32_32x32x16_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0,
+                                                     0);
+    }
+    static __device__ i32x16 mul32x2(u32x4 a, A b0, A b1, i32x16 c) {   // 32 columns
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
                                                      i32x4{(int)b0.x, (int)b0.y, (int)b1.x, (int)b1.y}, c, 0, 0, 0);
     }
 };
@@ -202,9 +220,14 @@ __device__ inline void load_to_lds(const void* from, void* to) {
 __device__ inline void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Tokens laid out for the products, in the workspace: 16-byte units, ordered,
-// [16 tokens][kt][PIECES][64 lanes] -- a piece of 1 KiB is one load of a wave --
-// and for 16 bits -1.5 2^-8 times each group's sum of each token, [64 tokens]
-// [kt][4][groups][16 tokens].  Tokens past m and columns past k are zeros.
+// in pieces of 1 KiB, one load of a wave each, which lane takes which unit as
+// the instructions want it:
+//   few tokens, 16 x 16:  [16 tokens][kt][PIECES p][64 lanes]: lane 16 c + r
+//                         takes unit 4 p + c of token r;
+//   many, 32 x 32:        [32 tokens][kt][2 PIECES: 2 p + s][64 lanes]: lane
+//                         32 h + r takes unit 4 p + 2 h + s of token r.
+// For 16 bits also -1.5 2^-8 times each group's sum of each token, [64 tokens]
+// [kt][groups][64].  Tokens past m and columns past k are zeros.
 constexpr int LAID_TOKENS = 64;   // the workspace holds a multiple of these
 __host__ __device__ inline uint64_t laid_units(uint64_t m, uint64_t kt, uint64_t bytes) {
     return (m + LAID_TOKENS - 1) / LAID_TOKENS * LAID_TOKENS * kt * (8 * bytes);
@@ -220,7 +243,7 @@ __device__ inline float* laid_sums(const MatvecArgs& a) {
 
 constexpr uint64_t FEW_IN_ROWS = 8;   // tokens that are read from their rows
 
-int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, uint64_t blocks, hipStream_t s);   // of 16 tokens
+int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s);
 int launch_matmul_w4(const MatvecArgs& a, int x_type, int scale_type, uint32_t group, hipStream_t s);
 
 }  // namespace lecb
