@@ -69,12 +69,11 @@ struct MmTile {
     static constexpr int GROUPS = 128 / GROUP, PIECES = 2 * Tokens<X>::PIECES;
     static constexpr int SCALES = GROUPS * 4 * 16, LOADS = SCALES * sizeof(S) < 256 ? 1 : SCALES * sizeof(S) / 256;
     u32x4 x[2 * PIECES][64];
-    u32x4 words[WN][4][64];
     S scales[WN][LOADS * 256 / sizeof(S)];                // [4][groups][16 rows]
     float excess[Operand<X>::OFFSET ? GROUPS : 1][64];    // of each token
 };
 
-// Sends for one tile while the other is computed.  The compiler keeps the reads
+// Sends for a tile while another is computed.  The compiler keeps the reads
 // of `now` apart from the loads on their way to `next` for being told here that
 // the two are different memory: it would wait for those loads first otherwise.
 template <typename Tile, typename F>
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
     constexpr int WK = MM_WAVES / WN, GROUPS = 128 / GROUP, WORDS = GROUP / 32, PIECES = Tile::PIECES;
     constexpr int COLS = MM_ROWS * WN, PITCH = COLS + 8;   // outputs of a token; + 8: rows on other banks
     union Shared {
-        Tile tile[2][WK];
+        Tile tile[3][WK];
         float y[WK][LAID_TOKENS][PITCH];
     };
     __shared__ Shared sh;
@@ -112,32 +111,46 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
 
     // tiles past the last repeat it: their sums are not stored
     auto tile_row = [&](uint32_t j) -> uint64_t { return n0 + wn * 4 + j < a.nt ? n0 + wn * 4 + j : a.nt - 1; };
-    const u32x4* from_words[4];
+    // lane 32 h + r's words: row r of 32, columns 32 d + 16 h + 8 s ..
+    const u32x4* from_words[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) from_words[j] = a.tiles + tile_row(j) * a.kt * 64;
-    const char* from_scales[Tile::LOADS];   // four bytes of the four tiles' scales
+    for (int j = 0; j < 2; ++j) from_words[j] = a.tiles + tile_row(2 * j + r / 16) * a.kt * 64 + 32 * h + r % 16;
+    struct Words {
+        u32x4 v[2][2];
+    } words0, words1;
+    // the wave's four tiles' scales, four bytes a lane; within 4 GiB of the first's (kt < MM_TILES)
     constexpr uint32_t ROW = GROUPS * 16 * sizeof(S);
+    static_assert(3ull * MM_TILES * ROW < 1ull << 32, "offsets of scales");
+    const char* from_scales = reinterpret_cast<const char*>(a.scales) + tile_row(0) * a.kt * ROW;
+    uint32_t scale_offset[Tile::LOADS];
 #pragma unroll
     for (int q = 0; q < Tile::LOADS; ++q) {
         const uint32_t b = (q * 256 + lane * 4) % (4 * ROW);
-        from_scales[q] = reinterpret_cast<const char*>(a.scales) + tile_row(b / ROW) * a.kt * ROW + b % ROW;
+        scale_offset[q] = (uint32_t)(tile_row(b / ROW) - tile_row(0)) * a.kt * ROW + b % ROW;
     }
     const u32x4* from_x = laid_tokens(a) + (uint64_t)mb * a.kt * (2 * PIECES * 64);
     const float* from_excess = laid_sums<X>(a) + (uint64_t)mb * a.kt * (GROUPS * 64);
 
-    constexpr int SENDS = 2 * PIECES / WN + 4 + Tile::LOADS + (O::OFFSET ? 1 : 0);
+    auto fetch_words = [&](Words& w, uint32_t tk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) w.v[j][s] = from_words[j][(uint64_t)tk * 64 + s * 16];
+        asm volatile("" ::: "memory");   // here, not where they are needed
+    };
+    constexpr int SENDS = 2 * PIECES / WN + Tile::LOADS + (O::OFFSET ? 1 : 0);
     auto send = [&](uint32_t tk, Tile* tile, int i) __attribute__((always_inline)) {
-        constexpr int A = 2 * PIECES / WN, B = A + 4, C = B + Tile::LOADS;
+        constexpr int A = 2 * PIECES / WN, B = A + Tile::LOADS;
         if (i < A) {
             // piece p of the two blocks of 32 tokens, which lie a.kt tiles apart
             const uint32_t p = i * WN + wn;
-            load_to_lds<16>(from_x + ((uint64_t)(p / PIECES) * a.kt + tk) * (PIECES * 64) + p % PIECES * 64 + lane, tile->x[p]);
+            load_to_lds<16>(from_x + ((uint64_t)(p / PIECES) * a.kt + tk) * (PIECES * 64) + p % PIECES * 64, 16 * lane,
+                            tile->x[p]);
         } else if (i < B) {
-            load_to_lds<16>(from_words[i - A] + (uint64_t)tk * 64 + lane, tile->words[wn][i - A]);
-        } else if (i < C) {
-            load_to_lds<4>(from_scales[i - B] + (uint64_t)tk * ROW, &tile->scales[wn][(i - B) * (256 / sizeof(S))]);
+            load_to_lds<4>(from_scales + (uint64_t)tk * ROW, scale_offset[i - A],
+                           &tile->scales[wn][(i - A) * (256 / sizeof(S))]);
         } else {   // by several waves alike
-            load_to_lds<4>(from_excess + ((uint64_t)tk * GROUPS + wn % GROUPS) * 64 + lane, tile->excess[wn % GROUPS]);
+            load_to_lds<4>(from_excess + ((uint64_t)tk * GROUPS + wn % GROUPS) * 64, 4 * lane, tile->excess[wn % GROUPS]);
         }
     };
 
@@ -151,16 +164,12 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
 
     // A group's columns, then 32 rows of W: those words become numbers and the
     // rows before are scaled while the matrix instructions run.
-    auto step = [&](uint32_t tk, const Tile* now, Tile* next) __attribute__((always_inline)) {
-        const uint32_t ahead = tk + WK < a.kt ? tk + WK : a.kt - 1;   // past the last: sent again, not used
+    auto step = [&](uint32_t tk, const Words& words, Words& next_words, const Tile* now, Tile* next) __attribute__((always_inline)) {
+        const uint32_t ahead = tk + 2 * WK < a.kt ? tk + 2 * WK : a.kt - 1;   // past the last: sent again, not used
         typedef decltype(O::mul32({}, {}, {})) Acc;
         constexpr int N = sizeof(X) == 2 ? 2 * WORDS : WORDS == 1 ? 2 : WORDS;   // pieces of a group
         constexpr int UNITS = 2 * GROUPS;
-        u32x4 words[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) words[j][s] = now->words[wn][2 * j + r / 16][(2 * h + s) * 16 + r % 16];
+        fetch_words(next_words, tk + WK < a.kt ? tk + WK : a.kt - 1);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             u32x4 xo[2][N];
@@ -192,14 +201,14 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
                 if constexpr (sizeof(X) == 2) {
 #pragma unroll
                     for (int p = 0; p < N; ++p) {
-                        const u32x4 w = O::weights(words[j][p % 2][g * WORDS + p / 2]);
+                        const u32x4 w = O::weights(words.v[j][p % 2][g * WORDS + p / 2]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) acc[i] = O::mul32(xo[i][p], w, acc[i]);
                     }
                 } else if constexpr (WORDS == 1) {   // half a unit
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const u32x2 w = O::weights(words[j][p][g]);
+                        const u32x2 w = O::weights(words.v[j][p][g]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             acc[i] = O::mul32(g & 1 ? u32x2{xo[i][p].z, xo[i][p].w} : u32x2{xo[i][p].x, xo[i][p].y}, w, acc[i]);
@@ -207,8 +216,8 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
                 } else {
 #pragma unroll
                     for (int p = 0; p < N; ++p) {
-                        const u32x2 w0 = O::weights(words[j][p % 2][g * WORDS + p / 2 * 2]);
-                        const u32x2 w1 = O::weights(words[j][p % 2][g * WORDS + p / 2 * 2 + 1]);
+                        const u32x2 w0 = O::weights(words.v[j][p % 2][g * WORDS + p / 2 * 2]);
+                        const u32x2 w1 = O::weights(words.v[j][p % 2][g * WORDS + p / 2 * 2 + 1]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) acc[i] = O::mul32x2(xo[i][p], w0, w1, acc[i]);
                     }
@@ -222,24 +231,35 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
         }
     };
 
-    // Every wave takes the same number of steps; those past the last tile only wait.
+    // Every wave takes the same number of steps; those past the last tile only
+    // wait.  Tokens are sent for two tiles ahead, words fetched for one: when
+    // the words are there, all that was sent before them is too.
     const uint32_t steps = (a.kt + WK - 1) / WK;
     if (wk < a.kt) {
 #pragma unroll
         for (int q = 0; q < SENDS; ++q) send(wk, &sh.tile[0][wk], q);
+        fetch_words(words0, wk);
+#pragma unroll
+        for (int q = 0; q < SENDS; ++q) send(wk + WK < a.kt ? wk + WK : a.kt - 1, &sh.tile[1][wk], q);
     }
-    for (uint32_t s = 0; s < steps; ++s) {
-        const uint32_t tk = s * WK + wk;
-        loads_done();
+    uint32_t tk = wk, b = 0;
+    auto turn = [&](const Words& words, Words& next_words) __attribute__((always_inline)) {
+        loads_done<SENDS>();
         lds_barrier();   // this tile is there, and the last one is read
         if (tk < a.kt)
-            mm_step<Tile>(&sh.tile[s & 1][wk], &sh.tile[(s + 1) & 1][wk],
-                          [&](const Tile* now, Tile* next) __attribute__((always_inline)) { step(tk, now, next); });
+            mm_step<Tile>(&sh.tile[b][wk], &sh.tile[b == 0 ? 2 : b - 1][wk],
+                          [&](const Tile* now, Tile* next) __attribute__((always_inline)) { step(tk, words, next_words, now, next); });
+        tk += WK;
+        b = b == 2 ? 0 : b + 1;
+    };
+    for (uint32_t s = 0; s < steps; s += 2) {
+        turn(words0, words1);
+        if (s + 1 < steps) turn(words1, words0);
     }
 
     // The columns' shares are added up in a fixed order, and a lane stores four
     // neighbouring outputs.
-    loads_done();
+    loads_done<0>();
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < 2; ++i)

@@ -262,8 +262,7 @@ int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s
     return scale_type == LECB_BF16 ? go(__bf16()) : go(float());
 }
 
-// Whether the workgroups of 64 tokens fill the compute units.
-bool many(const MatvecArgs& a) { return a.m > 64; }
+bool many(const MatvecArgs& a) { return a.m > 64 && a.kt < MM_TILES; }
 
 }  // namespace
 

@@ -198,26 +198,25 @@ __device__ inline void store_y(const MatvecArgs& a, uint64_t token, uint64_t col
 }
 
 // Waits for this wave's LDS accesses and then for the other waves.  Loads from
-// memory to registers stay in flight.
-__device__ inline void lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
+// memory stay in flight, those on their way to LDS too.
+__device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// BYTES (4 or 16) from each lane's address straight to LDS, lane after lane
-// from `to` on (the same in every lane); there after loads_done and, for the
-// other waves, a barrier.
+// BYTES (4 or 16) from `from` (the same in every lane) plus each lane's offset
+// straight to LDS, lane after lane from `to` on; there after loads_done and, for
+// the other waves, a barrier.  The buffer form: after a global one the compiler
+// waits for everything in flight at the next load it needs.
 template <int BYTES>
-__device__ inline void load_to_lds(const void* from, void* to) {
-    typedef const __attribute__((address_space(1))) void* Global;
+__device__ inline void load_to_lds(const void* from, uint32_t offset, void* to) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(from), 0, 0xffffffffu, 0x00020000);
     typedef __attribute__((address_space(3))) void* Lds;
     if constexpr (BYTES == 16)   // the builtin takes no dependent size
-        __builtin_amdgcn_global_load_lds((Global)from, (Lds)to, 16, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds)to, 16, offset, 0, 0, 0);
     else
-        __builtin_amdgcn_global_load_lds((Global)from, (Lds)to, 4, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds)to, 4, offset, 0, 0, 0);
 }
-__device__ inline void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for all of this wave's loads but the last N.
+template <int N>
+__device__ inline void loads_done() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 // Tokens laid out for the products, in the workspace: 16-byte units, ordered,
 // in pieces of 1 KiB, one load of a wave each, which lane takes which unit as
@@ -244,6 +243,7 @@ __device__ inline float* laid_sums(const MatvecArgs& a) {
 constexpr uint64_t FEW_IN_ROWS = 8;   // tokens that are read from their rows
 
 int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s);
+constexpr uint32_t MM_TILES = 1u << 22;   // more tiles of columns than this: in the form for few tokens
 int launch_matmul_w4(const MatvecArgs& a, int x_type, int scale_type, uint32_t group, hipStream_t s);
 
 }  // namespace lecb
