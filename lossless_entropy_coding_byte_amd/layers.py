@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from . import LecbError, _check, _ptr, _stream, load  # noqa: F401
+from . import _check, load
 
 LECB_F32, LECB_BF16, LECB_F16, LECB_I8 = 0, 1, 2, 3
 NORM_MAX_COLS = 32768
@@ -29,6 +29,19 @@ def _type(dtype, allowed, what):
     if dtype not in allowed:
         raise ValueError(f"{what}: {dtype} is not one of {', '.join(str(d) for d in allowed)}")
     return _TYPES[dtype]
+
+
+# A call on small tensors lasts as long as the host takes for it, so these two
+# are plain numbers, and the current stream is asked for by its handle: making
+# a Stream object of it takes 2.9 us, the handle 0.2 us.
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # --------------------------------------------------------------------------- the C ABI, one to one
@@ -85,11 +98,18 @@ def lecb_matvec_w4(x, x_stride, x_scale, x_scale_stride, m, tiles, scales, group
 
 # --------------------------------------------------------------------------- tensors
 
-def _here(*tensors):
+def _here(x, *tensors):
     """Checks that every tensor is on the current device."""
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+    here = torch.cuda.current_device() if x.is_cuda else None
+    for t in (x, *tensors):
+        if t is not None and t.get_device() != here:   # -1: host memory
             raise ValueError(f"tensor on {t.device}: the current GPU's memory is needed")
+
+
+def _like(x, dtype):
+    """A new tensor of x's shape with rows side by side."""
+    # empty_like takes 1.2 us, new_empty 1.8; it keeps other orders of dimensions, which must not get here
+    return torch.empty_like(x, dtype=dtype) if x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
 
 
 def _rows_of(x, what):
@@ -147,8 +167,8 @@ def quantize_w4(w, group: int = 128, scale_dtype=torch.bfloat16) -> W4Weights:
     n, k, stride = _rows_of(w, "quantize_w4")
     _here(w)
     nt, kt = -(-n // 16), -(-k // 128)
-    tiles = torch.empty((nt, kt, 1024), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((nt, kt * (128 // group), 16), dtype=scale_dtype, device=w.device)
+    tiles = w.new_empty((nt, kt, 1024), dtype=torch.uint8)
+    scales = w.new_empty((nt, kt * (128 // group), 16), dtype=scale_dtype)
     lecb_quantize_w4(w, stride, n, k, group, tiles, scales)
     return W4Weights(tiles, scales, n, k, group)
 
@@ -157,7 +177,7 @@ def dequantize_w4(w4: W4Weights, dtype=torch.bfloat16):
     """The weights [n, k] that the codes stand for."""
     _type(dtype, _FLOATS, "dequantize_w4")
     _here(w4.tiles, w4.scales)
-    out = torch.empty((w4.n, w4.k), dtype=dtype, device=w4.tiles.device)
+    out = w4.tiles.new_empty((w4.n, w4.k), dtype=dtype)
     lecb_dequantize_w4(w4.tiles, w4.scales, w4.group, w4.n, w4.k, out, w4.k)
     return out
 
@@ -167,7 +187,7 @@ def tile_w4(rows, n: int, k: int):
     if rows.dtype != torch.uint8 or n < 1 or k < 1 or rows.numel() != n * ((k + 1) // 2) or not rows.is_contiguous():
         raise ValueError("tile_w4: n * ceil(k / 2) contiguous uint8 are needed")
     _here(rows)
-    tiles = torch.empty((-(-n // 16), -(-k // 128), 1024), dtype=torch.uint8, device=rows.device)
+    tiles = rows.new_empty((-(-n // 16), -(-k // 128), 1024))
     lecb_tile_w4(rows, n, k, tiles)
     return tiles
 
@@ -178,7 +198,7 @@ def untile_w4(tiles, n: int, k: int):
             or tiles.numel() != -(-n // 16) * -(-k // 128) * 1024):
         raise ValueError("untile_w4: the contiguous uint8 tiles of [n, k] are needed")
     _here(tiles)
-    rows = torch.empty((n, (k + 1) // 2), dtype=torch.uint8, device=tiles.device)
+    rows = tiles.new_empty((n, (k + 1) // 2))
     lecb_untile_w4(tiles, n, k, rows)
     return rows
 
@@ -204,19 +224,19 @@ def rmsnorm_q8(x, weight, residual=None, eps: float = 1e-6, scale=None, out_h=No
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError("rmsnorm_q8: residual has x's shape and type")
         _, _, rs = _rows_of(residual, "rmsnorm_q8: residual")
-        h = out_h if out_h is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = out_h if out_h is not None else _like(x, x.dtype)
         if h.shape != x.shape or h.dtype != x.dtype:
             raise ValueError("rmsnorm_q8: out_h has x's shape and type")
         _, _, hs = _rows_of(h, "rmsnorm_q8: out_h")
     elif out_h is not None:
         raise ValueError("rmsnorm_q8: without a residual h is x")
     if scale is None:
-        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        s = x.new_empty(x.shape[:-1], dtype=torch.float32)
     else:
         s = scale
         if s.dtype != torch.float32 or s.numel() != 1:
             raise ValueError("rmsnorm_q8: a fixed scale is one float32 number")
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    q = _like(x, torch.int8)
     lecb_rmsnorm_q8(x, xs, residual, rs, weight, rows, cols, eps, h, hs, q, s, scale is not None)
     return q, s, (x if h is None else h)
 
@@ -231,7 +251,7 @@ def dequantize_q8(q, scale, dtype=torch.bfloat16):
     if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() not in (1, rows):
         raise ValueError("dequantize_q8: one float32 scale per row, or one")
     _here(q, scale)
-    out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    out = _like(q, dtype)
     lecb_dequantize_q8(q, rows, cols, scale, int(scale.numel() != 1), out)
     return out
 
@@ -256,9 +276,9 @@ def matvec_w4(x, w4: W4Weights, x_scale=None, out_dtype=None, ws=None):
     dtype = out_dtype if out_dtype is not None else torch.bfloat16 if is_int else x.dtype
     _type(dtype, _FLOATS, "matvec_w4: out_dtype")
     _here(x, w4.tiles, w4.scales, x_scale, ws)
-    y = torch.empty((*x.shape[:-1], w4.n), dtype=dtype, device=x.device)
+    y = x.new_empty((*x.shape[:-1], w4.n), dtype=dtype)
     if ws is None:
         need = lecb_matvec_w4_workspace_bytes(m, w4.n, w4.k)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        ws = x.new_empty(need, dtype=torch.uint8) if need else None
     lecb_matvec_w4(x, xs, x_scale, step, m, w4.tiles, w4.scales, w4.group, w4.n, w4.k, y, w4.n, ws)
     return y
