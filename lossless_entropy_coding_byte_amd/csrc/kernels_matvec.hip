@@ -20,15 +20,42 @@ struct Sums {
     f32x4 sum[MT][NT];
     Acc acc[MT][NT];
 
-    struct Weights {   // a tile's words and scales
+    // A tile's words and scales.  Loads are what a compute unit runs out of (one
+    // in about 25 cycles, whatever its width), so four scales of a row of W come
+    // in one load, one to each 16 lanes, and are handed around in registers:
+    // scale (j, g) is number GROUPS j + g.
+    static constexpr int COUNT = NT * GROUPS, EACH = COUNT < 4 ? COUNT : 4, LOADS = COUNT / EACH;
+    struct Weights {
         u32x4 words[NT];
-        S scale[NT][GROUPS];
+        S raw[LOADS];
+        float scale[COUNT];
         __device__ void load(const u32x4* const* tiles, const S* const* scales, uint32_t tk, uint32_t lane) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                words[j] = __builtin_nontemporal_load(tiles[j] + (uint64_t)tk * 64 + lane);
+            for (int j = 0; j < NT; ++j) words[j] = __builtin_nontemporal_load(tiles[j] + (uint64_t)tk * 64 + lane);
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) scale[j][g] = (scales[j] + ((uint64_t)tk * GROUPS + g) * 16)[lane & 15];
+            for (int q = 0; q < LOADS; ++q) raw[q] = scales[q][(uint64_t)tk * (GROUPS * 16)];
+        }
+        __device__ void spread() {
+#pragma unroll
+            for (int q = 0; q < LOADS; ++q) {
+                const uint32_t v = __float_as_uint((float)raw[q]);
+                if constexpr (EACH == 1) {
+                    scale[q] = __uint_as_float(v);
+                } else {
+                    // rows of 16 lanes 0 1 2 3 -> 0 0 2 2 and 1 1 3 3 -> each everywhere
+                    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+                    if constexpr (EACH == 2) {
+                        scale[2 * q] = __uint_as_float(p[0]);
+                        scale[2 * q + 1] = __uint_as_float(p[1]);
+                    } else {
+                        const auto a = __builtin_amdgcn_permlane32_swap(p[0], p[0], false, false);
+                        const auto b = __builtin_amdgcn_permlane32_swap(p[1], p[1], false, false);
+                        scale[4 * q] = __uint_as_float(a[0]);
+                        scale[4 * q + 1] = __uint_as_float(b[0]);
+                        scale[4 * q + 2] = __uint_as_float(a[1]);
+                        scale[4 * q + 3] = __uint_as_float(b[1]);
+                    }
+                }
             }
         }
     };
@@ -57,7 +84,7 @@ struct Sums {
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         const u32x2 x = d ? u32x2{h.x[i][0].z, h.x[i][0].w} : u32x2{h.x[i][0].x, h.x[i][0].y};
-                        finish(i, j, O::mul(x, q, Acc{0, 0, 0, 0}), (float)w.scale[j][2 * H + d]);
+                        finish(i, j, O::mul(x, q, Acc{0, 0, 0, 0}), w.scale[j * GROUPS + 2 * H + d]);
                     }
                 }
         } else if constexpr (sizeof(X) == 1) {
@@ -68,7 +95,7 @@ struct Sums {
                 for (int i = 0; i < MT; ++i)
                     acc[i][j] = O::mul2(h.x[i][0], q0, q1, WORDS == 4 && H == 1 ? acc[i][j] : Acc{0, 0, 0, 0});
                 if constexpr (WORDS == 2 || H == 1) {
-                    const float s = (float)w.scale[j][H * GROUPS / 2];
+                    const float s = w.scale[j * GROUPS + H * GROUPS / 2];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) finish(i, j, acc[i][j], s);
                 }
@@ -90,7 +117,7 @@ struct Sums {
                     u32x4 q[N];
 #pragma unroll
                     for (int d = 0; d < N; ++d) q[d] = O::weights(w.words[j][2 * H + g * N + d]);
-                    const float s = (float)w.scale[j][WORDS == 4 ? 0 : H * GROUPS / 2 + g];
+                    const float s = w.scale[j * GROUPS + (WORDS == 4 ? 0 : H * GROUPS / 2 + g)];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         Acc v = WORDS == 4 && H == 1 ? acc[i][j] : none[i];
@@ -108,97 +135,194 @@ struct Sums {
     }
 };
 
+// A wave's tiles, every `waves`-th from `wave` on: fetch(d, tile) for DEPTH of
+// them ahead of add(d).  Past its last tile a wave fetches that one again.
+template <int DEPTH, typename Fetch, typename Add>
+__device__ __forceinline__ void run(uint32_t wave, uint32_t waves, uint32_t tiles, Fetch fetch, Add add) {
+    if (wave >= tiles) return;
+    const uint32_t mine = (tiles - wave + waves - 1) / waves;
+    auto tile = [&](uint32_t t) { return wave + (t < mine ? t : mine - 1) * waves; };
+    uint32_t t = 0;
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) fetch(d, tile(d));
+    for (; t + DEPTH < mine; t += DEPTH)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            add(d);
+            __builtin_amdgcn_sched_barrier(0);   // mixed, the tiles' work runs out of registers
+            fetch(d, tile(t + DEPTH + d));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        if (t + d < mine) {
+            add(d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
 // Waves of a workgroup: as many as the registers leave room for.
 constexpr int few_waves(int mt, int nt) { return mt * nt == 1 ? 16 : 8; }
+// Tiles that a wave has on their way or in registers.
+constexpr int few_depth(int mt, int nt) { return nt == 4 ? 2 : mt == 2 ? 5 - nt : nt == 1 ? 4 : 3; }
 
-// One workgroup: 16 NT rows of W times 16 MT tokens.  Its waves share the
-// columns out, tile by tile, each with the next tile's words and the next
-// half's tokens in flight while it works on one, and add their sums up in LDS
-// in a fixed order.
-template <typename X, typename S, int GROUP, int MT, int NT, bool LAID>
+// Tokens of their rows' tile, few enough that the 16 lanes of an instruction's
+// tokens load several words' columns at once: lane 16 c + r takes eight columns
+// of token r % ROWS; for word d they are then moved to lanes r < ROWS.
+template <typename X, int ROWS>
+struct InRows {
+    typedef Operand<X> O;
+    typedef typename O::A A;
+    static constexpr int LOADS = ROWS / 4, PER = 16 / ROWS;   // words a load
+    A v[LOADS];
+    static __device__ uint32_t column(int i, uint32_t r, uint32_t c) { return 32 * (i * PER + r / ROWS) + 8 * c; }
+    __device__ void load(const X* tile, uint32_t r, uint32_t c) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) v[i] = load_eight(tile, column(i, r, c));
+    }
+    __device__ void load(const X* tile, uint32_t r, uint32_t c, uint32_t left) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) v[i] = load_eight(tile, column(i, r, c), left);
+    }
+    __device__ void order() {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) v[i] = O::order(v[i]);
+    }
+    template <int D>
+    __device__ A word() const {
+        A a = v[D / PER];
+        constexpr int FROM = D % PER * ROWS;   // lane r takes lane r + FROM of its sixteen
+        if constexpr (FROM > 0) {
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(A) / 4); ++i)
+                a[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a[i], 0x120 + 16 - FROM, 0xf, 0xf, true);
+        }
+        return a;
+    }
+    template <int H, typename Half>
+    __device__ void half(Half& h) const {
+        if constexpr (sizeof(X) == 1) {
+            h.x[0][0] = Tokens<X>::join(word<2 * H>(), word<2 * H + 1>());
+        } else {
+            h.x[0][0] = word<2 * H>();
+            h.x[0][1] = word<2 * H + 1>();
+        }
+    }
+};
+
+// One workgroup: 16 NT rows of W times 16 MT tokens, laid out (ROWS = 0), or
+// times ROWS tokens in their rows.  Its waves share the columns out, tile by
+// tile, each with the next tiles' loads in flight while it works on one, and
+// add their sums up in LDS in a fixed order.  (64 tokens' tiles are too large
+// for that: their words are one tile ahead, tokens half of one.)
+template <typename X, typename S, int GROUP, int MT, int NT, int ROWS>
 __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(MatvecArgs a) {
     typedef Operand<X> O;
     typedef Tokens<X> T;
     typedef Sums<X, S, GROUP, MT, NT> Su;
-    static_assert(LAID || MT == 1, "tokens in rows: 16 at most");
+    static_assert(ROWS == 0 || MT == 1, "tokens in rows: 8 at most");
     constexpr int COLS = 16 * NT, PITCH = COLS + 4;   // outputs of a token; + 4: rows on other banks
-    __shared__ float part[few_waves(MT, NT)][16 * MT][PITCH];
+    constexpr int TOKENS = ROWS ? ROWS : 16 * MT;
+    __shared__ float part[few_waves(MT, NT)][TOKENS][PITCH];
     const uint32_t waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
     const uint32_t n0 = blockIdx.x * NT, mt0 = blockIdx.y * MT;
+    // tiles past the last repeat it: their sums are not stored
+    auto tile_row = [&](uint32_t j) -> uint64_t { return n0 + j < a.nt ? n0 + j : a.nt - 1; };
     const u32x4* tiles[NT];
-    const S* scales[NT];
+    const S* scales[Su::LOADS];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {   // tiles past the last repeat it: their sums are not stored
-        const uint64_t tn = n0 + j < a.nt ? n0 + j : a.nt - 1;
-        tiles[j] = a.tiles + tn * a.kt * 64;
-        scales[j] = reinterpret_cast<const S*>(a.scales) + tn * a.kt * (Su::GROUPS * 16);
-    }
-    const u32x4* laid[MT];
-    const X* row = nullptr;
-    if constexpr (LAID) {
-        const uint32_t last = (uint32_t)((a.m - 1) / 16);   // so do tokens past the last sixteen
+    for (int j = 0; j < NT; ++j) tiles[j] = a.tiles + tile_row(j) * a.kt * 64;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            laid[i] = laid_tokens(a) + (uint64_t)(mt0 + i < last ? mt0 + i : last) * a.kt * (T::PIECES * 64);
-    } else {
-        row = reinterpret_cast<const X*>(a.x) + (r < a.m ? r : a.m - 1) * a.x_stride;
+    for (int q = 0; q < Su::LOADS; ++q) {
+        const uint32_t i = q * Su::EACH + c % Su::EACH;   // this lane's scale
+        scales[q] = reinterpret_cast<const S*>(a.scales) + tile_row(i / Su::GROUPS) * a.kt * (Su::GROUPS * 16) +
+                    i % Su::GROUPS * 16 + r;
     }
     Su sums;
     sums.clear();
-    const uint32_t whole = LAID ? a.kt : (uint32_t)(a.k / TILE_COLS);
-    auto load = [&](typename Su::Half& h, uint32_t tk, uint32_t half) {
+    if constexpr (ROWS > 0) {
+        constexpr int DEPTH = few_depth(MT, NT);
+        typedef InRows<X, ROWS> Rows;
+        const X* row = reinterpret_cast<const X*>(a.x) + (r % ROWS < a.m ? r % ROWS : a.m - 1) * a.x_stride;
+        const uint32_t whole = (uint32_t)(a.k / TILE_COLS);
+        typename Su::Weights w[DEPTH];
+        Rows x[DEPTH];
+        auto add = [&](typename Su::Weights& ww, Rows& xx) {
+            typename Su::Half h;
+            ww.spread();
+            xx.order();
+            xx.template half<0>(h);
+            sums.template add<0>(ww, h);
+            xx.template half<1>(h);
+            sums.template add<1>(ww, h);
+        };
+        run<DEPTH>(
+            wave, waves, whole,
+            [&](int d, uint32_t tk) {
+                x[d].load(row + (uint64_t)tk * TILE_COLS, r, c);
+                w[d].load(tiles, scales, tk, lane);
+            },
+            [&](int d) { add(w[d], x[d]); });
+        if (whole < a.kt && wave == whole % waves) {   // the columns that do not fill a tile
+            x[0].load(row + (uint64_t)whole * TILE_COLS, r, c, (uint32_t)(a.k % TILE_COLS));
+            w[0].load(tiles, scales, whole, lane);
+            add(w[0], x[0]);
+        }
+    } else {
+        const u32x4* laid[MT];
+        const uint32_t last = (uint32_t)((a.m - 1) / 16);   // tokens past the last sixteen repeat them
 #pragma unroll
         for (int i = 0; i < MT; ++i)
+            laid[i] = laid_tokens(a) + (uint64_t)(mt0 + i < last ? mt0 + i : last) * a.kt * (T::PIECES * 64);
+        auto load = [&](typename Su::Half& h, uint32_t tk, uint32_t half) {
 #pragma unroll
-            for (int p = 0; p < Su::HALF; ++p) {
-                if constexpr (LAID)
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int p = 0; p < Su::HALF; ++p)
                     h.x[i][p] = (laid[i] + ((uint64_t)tk * T::PIECES + half * Su::HALF + p) * 64)[lane];
-                else
-                    h.x[i][p] = T::load(row + (uint64_t)tk * TILE_COLS, 4 * (half * Su::HALF + p) + c);
+        };
+        if constexpr (MT <= 2) {
+            constexpr int DEPTH = few_depth(MT, NT);
+            typename Su::Weights w[DEPTH];
+            typename Su::Half h[DEPTH][2];
+            run<DEPTH>(
+                wave, waves, a.kt,
+                [&](int d, uint32_t tk) {
+                    load(h[d][0], tk, 0);
+                    load(h[d][1], tk, 1);
+                    w[d].load(tiles, scales, tk, lane);
+                },
+                [&](int d) {
+                    w[d].spread();
+                    sums.template add<0>(w[d], h[d][0]);
+                    sums.template add<1>(w[d], h[d][1]);
+                });
+        } else {
+            typename Su::Weights w0, w1;
+            typename Su::Half h0, h1;
+            uint32_t tk = wave;
+            if (tk < a.kt) {
+                load(h0, tk, 0);
+                w0.load(tiles, scales, tk, lane);
             }
-    };
-    auto ordered = [&](typename Su::Half h) {
-        if constexpr (!LAID) {
-#pragma unroll
-            for (int p = 0; p < Su::HALF; ++p) h.x[0][p] = O::order(h.x[0][p]);
-        }
-        return h;
-    };
-    typename Su::Weights w0, w1;
-    typename Su::Half h0, h1;
-    uint32_t tk = wave;
-    if (tk < whole) {
-        load(h0, tk, 0);
-        w0.load(tiles, scales, tk, lane);
-    }
-    while (tk < whole) {
-        const uint32_t t1 = tk + waves, t2 = t1 + waves;
-        load(h1, tk, 1);
-        if (t1 < whole) w1.load(tiles, scales, t1, lane);
-        sums.template add<0>(w0, ordered(h0));
-        if (t1 < whole) load(h0, t1, 0);
-        sums.template add<1>(w0, ordered(h1));
-        if (t1 >= whole) break;
-        load(h1, t1, 1);
-        if (t2 < whole) w0.load(tiles, scales, t2, lane);
-        sums.template add<0>(w1, ordered(h0));
-        if (t2 < whole) load(h0, t2, 0);
-        sums.template add<1>(w1, ordered(h1));
-        tk = t2;
-    }
-    if constexpr (!LAID) {
-        if (whole < a.kt && wave == whole % waves) {   // the columns that do not fill a tile
-            const X* p = row + (uint64_t)whole * TILE_COLS;
-            const uint32_t left = (uint32_t)(a.k % TILE_COLS);
-            w0.load(tiles, scales, whole, lane);
-#pragma unroll
-            for (int i = 0; i < Su::HALF; ++i) {
-                h0.x[0][i] = T::load(p, 4 * i + c, left);
-                h1.x[0][i] = T::load(p, 4 * (Su::HALF + i) + c, left);
+            while (tk < a.kt) {
+                const uint32_t t1 = tk + waves, t2 = t1 + waves;
+                load(h1, tk, 1);
+                if (t1 < a.kt) w1.load(tiles, scales, t1, lane);
+                w0.spread();
+                sums.template add<0>(w0, h0);
+                if (t1 < a.kt) load(h0, t1, 0);
+                sums.template add<1>(w0, h1);
+                if (t1 >= a.kt) break;
+                load(h1, t1, 1);
+                if (t2 < a.kt) w0.load(tiles, scales, t2, lane);
+                w1.spread();
+                sums.template add<0>(w1, h0);
+                if (t2 < a.kt) load(h0, t2, 0);
+                sums.template add<1>(w1, h1);
+                tk = t2;
             }
-            sums.template add<0>(w0, ordered(h0));
-            sums.template add<1>(w0, ordered(h1));
         }
     }
 #pragma unroll
@@ -206,10 +330,11 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * c + e][16 * j + r] = sums.sum[i][j][e];
+            for (int e = 0; e < 4; ++e)
+                if (16 * i + 4 * c + e < TOKENS) part[wave][16 * i + 4 * c + e][16 * j + r] = sums.sum[i][j][e];
     lds_barrier();
     // the lanes of all waves share the outputs out, four neighbours each
-    for (uint32_t at = threadIdx.x; at < MT * 16 * COLS / 4; at += blockDim.x) {
+    for (uint32_t at = threadIdx.x; at < TOKENS * COLS / 4; at += blockDim.x) {
         const uint32_t t = at / (COLS / 4), n = at % (COLS / 4) * 4;
         const uint64_t token = (uint64_t)mt0 * 16 + t, col = (uint64_t)n0 * 16 + n;
         if (token >= a.m || col >= a.n) continue;
@@ -219,13 +344,15 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
     }
 }
 
-template <typename X, typename S, int GROUP, int MT, int NT, bool LAID>
+template <typename X, typename S, int GROUP, int MT, int NT, int ROWS>
 int launch_few(const MatvecArgs& a, hipStream_t s) {
     const uint64_t mt = tiles_of(a.m, 16 * MT);
     if (mt > 65535) return LECB_ERR_TOO_LARGE;
-    uint32_t waves = few_waves(MT, NT);   // no more than there are tiles to share
-    while (waves > 1 && waves / 2 >= a.kt) waves /= 2;
-    matvec_w4_kernel<X, S, GROUP, MT, NT, LAID>
+    // No more waves than have DEPTH tiles each, but four: what a wave asks for past
+    // its last tile costs loads, a wave more only a share of the last sums.
+    uint32_t waves = few_waves(MT, NT);
+    while (waves > 4 && waves * few_depth(MT, NT) > a.kt) waves /= 2;
+    matvec_w4_kernel<X, S, GROUP, MT, NT, ROWS>
         <<<dim3((uint32_t)tiles_of(a.nt, NT), (uint32_t)mt), waves * 64, 0, s>>>(a);
     return launched();
 }
@@ -235,20 +362,21 @@ int launch_group(const MatvecArgs& a, hipStream_t s) {
     // More rows of W for a wave spare loads of x, fewer make more workgroups:
     // as many as leave one workgroup per compute unit.
     const uint32_t cus = (uint32_t)device_cu_count();
-    auto go = [&](auto mt, auto laid) -> int {
-        constexpr int MT = decltype(mt)::value;
-        constexpr bool LAID = decltype(laid)::value;
+    auto go = [&](auto mt, auto in_rows) -> int {
+        constexpr int MT = decltype(mt)::value, ROWS = decltype(in_rows)::value;
         const uint64_t rows = a.nt * tiles_of(a.m, 16 * MT);
         if constexpr (MT < 4) {
-            if (rows >= 4 * cus) return launch_few<X, S, GROUP, MT, 4, LAID>(a, s);
+            if (rows >= 4 * cus) return launch_few<X, S, GROUP, MT, 4, ROWS>(a, s);
         }
-        if (rows >= 2 * cus) return launch_few<X, S, GROUP, MT, 2, LAID>(a, s);
-        return launch_few<X, S, GROUP, MT, 1, LAID>(a, s);
+        if (rows >= 2 * cus) return launch_few<X, S, GROUP, MT, 2, ROWS>(a, s);
+        return launch_few<X, S, GROUP, MT, 1, ROWS>(a, s);
     };
-    if (a.m <= FEW_IN_ROWS) return go(std::integral_constant<int, 1>(), std::false_type());
-    if (a.m <= 16) return go(std::integral_constant<int, 1>(), std::true_type());
-    if (a.m <= 32) return go(std::integral_constant<int, 2>(), std::true_type());
-    return go(std::integral_constant<int, 4>(), std::true_type());
+    typedef std::integral_constant<int, 0> Laid;
+    if (a.m <= 4) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
+    if (a.m <= FEW_IN_ROWS) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+    if (a.m <= 16) return go(std::integral_constant<int, 1>(), Laid());
+    if (a.m <= 32) return go(std::integral_constant<int, 2>(), Laid());
+    return go(std::integral_constant<int, 4>(), Laid());
 }
 
 template <typename X>

@@ -96,10 +96,12 @@ struct Operand<int8_t> {
     static constexpr float FACTOR = 0.0625f;
     static constexpr bool OFFSET = false;
     static __device__ A weights(uint32_t w) { return {(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u}; }
-    // two times eight bytes
-    static __device__ u32x4 order(u32x4 x) {
-        return {__builtin_amdgcn_perm(x.y, x.x, 0x06040200u), __builtin_amdgcn_perm(x.y, x.x, 0x07050301u),
-                __builtin_amdgcn_perm(x.w, x.z, 0x06040200u), __builtin_amdgcn_perm(x.w, x.z, 0x07050301u)};
+    static __device__ u32x2 order(u32x2 x) {
+        return {__builtin_amdgcn_perm(x.y, x.x, 0x06040200u), __builtin_amdgcn_perm(x.y, x.x, 0x07050301u)};
+    }
+    static __device__ u32x4 order(u32x4 x) {   // two times eight bytes
+        const u32x2 a = order(u32x2{x.x, x.y}), b = order(u32x2{x.z, x.w});
+        return {a.x, a.y, b.x, b.y};
     }
     static __device__ Acc mul(A a, A b, Acc c) {
         return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0,
@@ -120,6 +122,28 @@ struct Operand<int8_t> {
     }
 };
 
+// Eight neighbouring entries of a token's tile (8 sizeof(X) bytes), in order;
+// of the first `left` (at least one) columns only, zeros after them: entries
+// past them repeat the last one's load, so that all are in flight at once.
+template <typename X>
+__device__ inline typename Operand<X>::A load_eight(const X* tile, uint32_t col) {
+    typedef typename Operand<X>::A any __attribute__((aligned(sizeof(X))));
+    return *reinterpret_cast<const any*>(tile + col);
+}
+template <typename X>
+__device__ inline typename Operand<X>::A load_eight(const X* tile, uint32_t col, uint32_t left) {
+    constexpr int PER = 4 / sizeof(X), BITS = 8 * sizeof(X);
+    typename Operand<X>::A v{};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t at = col + i < left ? col + i : left - 1;
+        const uint32_t e = sizeof(X) == 1 ? reinterpret_cast<const uint8_t*>(tile)[at]
+                                          : reinterpret_cast<const uint16_t*>(tile)[at];
+        v[i / PER] |= (col + i < left ? e : 0u) << (BITS * (i % PER));
+    }
+    return v;
+}
+
 // A token's 128 columns of a tile as 16-byte units, each what a lane gives one
 // instruction of 16 bits or of 64 columns of bytes: 16 bits, unit u holds
 // columns 8 u ..; bytes, unit 4 p + c holds columns 64 p + 8 c .. and 64 p + 32
@@ -127,31 +151,22 @@ struct Operand<int8_t> {
 template <typename X>
 struct Tokens {
     static constexpr int PIECES = 2 * sizeof(X), UNITS = 4 * PIECES;
-    typedef u32x2 u32x2_any __attribute__((aligned(1)));
-    typedef u32x4 u32x4_any __attribute__((aligned(1)));
+    static __device__ uint32_t column(uint32_t unit) {
+        return sizeof(X) == 1 ? 64 * (unit >> 2) + 8 * (unit & 3) : 8 * unit;
+    }
     static __device__ u32x4 load(const X* tile, uint32_t unit) {
-        if constexpr (sizeof(X) == 1) {
-            const X* p = tile + 64 * (unit >> 2) + 8 * (unit & 3);
-            const u32x2 a = *reinterpret_cast<const u32x2_any*>(p), b = *reinterpret_cast<const u32x2_any*>(p + 32);
-            return {a.x, a.y, b.x, b.y};
-        } else {
-            return *reinterpret_cast<const u32x4_any*>(tile + 8 * unit);
-        }
+        if constexpr (sizeof(X) == 1)
+            return join(load_eight(tile, column(unit)), load_eight(tile, column(unit) + 32));
+        else
+            return load_eight(tile, column(unit));
     }
-    // the tile's first `left` columns only, zeros after them
     static __device__ u32x4 load(const X* tile, uint32_t unit, uint32_t left) {
-        constexpr int N = 16 / sizeof(X), PER = 4 / sizeof(X), BITS = 8 * sizeof(X);
-        u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t c = sizeof(X) == 1 ? 64 * (unit >> 2) + 8 * (unit & 3) + 32 * (i / 8) + i % 8 : 8 * unit + i;
-            if (c >= left) continue;
-            const uint32_t e = sizeof(X) == 1 ? reinterpret_cast<const uint8_t*>(tile)[c]
-                                              : reinterpret_cast<const uint16_t*>(tile)[c];
-            v[i / PER] |= e << (BITS * (i % PER));
-        }
-        return v;
+        if constexpr (sizeof(X) == 1)
+            return join(load_eight(tile, column(unit), left), load_eight(tile, column(unit) + 32, left));
+        else
+            return load_eight(tile, column(unit), left);
     }
+    static __device__ u32x4 join(u32x2 a, u32x2 b) { return {a.x, a.y, b.x, b.y}; }
 };
 
 struct MatvecArgs {
