@@ -28,28 +28,34 @@ __device__ inline float product(float a, float b) {
 // ---------------------------------------------------------------- 4-bit weights
 
 // The step of a group and what turns weights into codes.  q = rint(w / s) of
-// the exact quotient: n = rint(w * (1/s)) is that or its neighbour (the
-// product is off by under two units in its last place), and e = w - n s is
-// exact (one fused operation, and both terms are multiples of the smaller
+// the exact quotient: with inv = 1 / s rounded, n = rint(w inv) is that or its
+// neighbour (w inv is off by under two units in its last place), and e = w - n s
+// is exact (one fused operation, and both terms are multiples of the smaller
 // one's last place within 24 bits of s), so comparing |e| with s / 2 settles
-// it.  Steps below 2^-60 work on s and w times 2^64, so that neither 1/s nor
-// s / 2 leaves the range.
+// it.  Eight weights at a time: what has to be settled is seen from the largest
+// |e| of the eight and is rare.  Not so for 16-bit weights with 16-bit steps,
+// one in some 700 of which lies half a step between two codes: those settle each
+// weight, by adding e / s to n in one more fused operation, with 1/s a little
+// smaller where n is even and larger where it is odd, so that half a step goes
+// to the even code; any other e differs from it by 2^-12 at least.
+//
+// Adding MAGIC to w inv, in one fused operation, rounds it to n and leaves n + 8
+// in the lowest four bits; shifted and added up, the eight make the word.
+// Steps that are not from 2^-60 to 2^100 go one by one, with s and w times 2^64
+// where they are small, so that neither 1/s nor s / 2 leaves the range.
 struct Step {
-    float s;      // as stored (0: all codes 0; NaN: not finite)
-    float t;      // s * lift
-    float inv;    // 1 / t, or 0
-    float lift;   // 1 or 2^64
+    float s;     // as stored (0: all codes 0; NaN: not finite)
+    float inv;   // 1 / s, of 2^64 s where s is small, 0 where it is 0 or NaN
+    __device__ static float lift(float s) { return s < 0x1p-60f ? 0x1p64f : 1.0f; }
     __device__ void set(uint32_t amax_bits, bool bf16) {
         s = amax_bits >= INF_BITS ? __uint_as_float(0x7fc00000u) : __uint_as_float(amax_bits) / 7.0f;
         if (bf16) s = (float)(__bf16)s;
         // a step that rounding to 16 bits carried to infinity is none either
         if (abs_bits(s) >= INF_BITS) s = __uint_as_float(0x7fc00000u);
-        lift = s < 0x1p-60f ? 0x1p64f : 1.0f;
-        t = s * lift;
-        inv = t > 0.0f ? 1.0f / t : 0.0f;
+        inv = s > 0.0f ? 1.0f / (s * lift(s)) : 0.0f;
     }
     __device__ uint32_t code(float w) const {
-        const float v = w * lift;
+        const float t = s * lift(s), v = w * lift(s);
         float n = rintf(v * inv);
         const float e = fmaf(-n, t, v), a = fabsf(e) + fabsf(e);
         const bool odd = ((int)n & 1) != 0;
@@ -57,58 +63,104 @@ struct Step {
         n = fminf(fmaxf(n, -7.0f), 7.0f);
         return inv > 0.0f ? (uint32_t)(int)n & 15u : 0u;
     }
+    template <typename P>
+    __device__ uint32_t word(const P& w, bool halves) const {   // halves: weights and step of 16 bits
+        constexpr float MAGIC = 12582920.0f;   // 1.5 2^23 + 8: 0x4b400008
+        uint32_t q = 0u - 0x4b400000u * 0x11111111u;
+        float worst = 0.0f;
+        if (halves) {
+            const uint32_t below = __float_as_uint(inv) - 4;   // units in the last place
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float m = fmaf(w[i], inv, MAGIC);
+                const float e = fmaf(MAGIC - m, s, w[i]);
+                m = fmaf(e, __uint_as_float(below + ((__float_as_uint(m) & 1u) << 3)), m);
+                q += __float_as_uint(m) << (4 * i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = fmaf(w[i], inv, MAGIC);
+                q += __float_as_uint(m) << (4 * i);
+                worst = fmaxf(worst, fabsf(fmaf(MAGIC - m, s, w[i])));
+            }
+        }
+        q ^= 0x88888888u;
+        if (!(worst + worst < s && s >= 0x1p-60f && s < 0x1p100f)) {
+            q = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q |= code(w[i]) << (4 * i);
+        }
+        return q;
+    }
 };
 
-// One wave makes one tile: lane 16 c + r takes row r, columns 32 d + 8 c .. + 7
-// for d = 0..3 -- the four words of its 16 bytes -- so a group's maximum needs
-// the lanes r, r + 16, r + 32, r + 48 only, and the tile leaves in one store.
+template <int CTRL>
+__device__ inline uint32_t max_lanes(uint32_t v) {   // of v and the v of the lane that CTRL names
+    return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
+}
+
+template <int I>
+__device__ inline float of_quad(float v) {   // lane I's of each four
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), I * 0x55, 0xf, 0xf, true));
+}
+
+// One wave makes one tile: four loads of four rows each, eight columns a lane,
+// so that rows are read in whole lines and a group's maximum is that of 4 to 16
+// neighbouring lanes.  Lane i of each four makes the step of load i's row, as the
+// two divisions cost as much as four weights' codes.  The words go through LDS
+// into the tile's order, so that it leaves in one store.
 template <typename T, int GROUP>
 __global__ __launch_bounds__(256) void quantize_w4_kernel(const T* __restrict__ w, uint64_t stride, uint64_t n,
                                                           uint64_t k, uint32_t kt, uint32_t tiles,
                                                           u32x4* __restrict__ out, void* __restrict__ scales,
                                                           int bf16) {
-    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int GROUPS = 128 / GROUP, LANES = GROUP / 8;
+    __shared__ __attribute__((aligned(16))) uint32_t s_words[4][4 * 80];   // [c][16 r][4 d], 16 words apart: other banks
+    __shared__ float s_scales[4][GROUPS * 16];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile = blockIdx.x * 4 + wave;
     if (tile >= tiles) return;
-    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+    const uint32_t lane = threadIdx.x & 63, u = lane & 15;
     const uint32_t tn = tile / kt, tk = tile % kt;
-    const uint64_t row = (uint64_t)tn * TILE_ROWS + r;
-    const uint64_t col = (uint64_t)tk * TILE_COLS + 8 * c;
+    const uint64_t col = (uint64_t)tk * TILE_COLS + 8 * u;
+    const uint64_t left = col < k ? k - col : 0;   // columns from `col` on
     Piece<T> v[4];
-    const uint64_t left = row < n && col < k ? k - col : 0;   // columns of this row from `col` on
-    const T* p = w + (left ? row * stride + col : 0);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) v[d].load(p + 32 * d, left > 32u * d ? left - 32u * d : 0);
-    constexpr int WORDS = GROUP / 32, GROUPS = 4 / WORDS;
-    u32x4 words;
-    float mine = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t row = (uint64_t)tn * TILE_ROWS + 4 * i + (lane >> 4);
+        const uint64_t have = row < n ? left : 0;
+        v[i].load(w + (have ? row * stride + col : 0), have);
+    }
+    uint32_t mine = 0;
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
+    for (int i = 0; i < 4; ++i) {
         uint32_t a = 0;
 #pragma unroll
-        for (int d = g * WORDS; d < (g + 1) * WORDS; ++d)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a = umax(a, abs_bits(v[d][i]));
-        a = umax(a, __shfl_xor(a, 16));
-        a = umax(a, __shfl_xor(a, 32));
-        Step st;
-        st.set(a, bf16);
-        if (c == (uint32_t)g) mine = st.s;
-#pragma unroll
-        for (int d = g * WORDS; d < (g + 1) * WORDS; ++d) {
-            uint32_t q = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q |= st.code(v[d][i]) << (4 * i);
-            words[d] = q;
-        }
+        for (int e = 0; e < 8; ++e) a = umax(a, abs_bits(v[i][e]));
+        a = max_lanes<0xB1>(a);                      // the next lane's
+        a = max_lanes<0x4E>(a);                      // the next two's
+        if (GROUP >= 64) a = max_lanes<0x141>(a);    // mirrored within eight
+        if (GROUP >= 128) a = max_lanes<0x140>(a);   // mirrored within sixteen
+        mine = (u & 3) == (uint32_t)i ? a : mine;
     }
-    out[(uint64_t)tile * 64 + lane] = words;
-    // lane 16 g + r holds the scale of group g, row r: the order they are stored in
-    if (c < (uint32_t)GROUPS) {
+    Step own;
+    own.set(mine, bf16);
+    const Step st[4] = {{of_quad<0>(own.s), of_quad<0>(own.inv)}, {of_quad<1>(own.s), of_quad<1>(own.inv)},
+                        {of_quad<2>(own.s), of_quad<2>(own.inv)}, {of_quad<3>(own.s), of_quad<3>(own.inv)}};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_words[wave][(u & 3) * 80 + (4 * i + (lane >> 4)) * 4 + (u >> 2)] =
+        st[i].word(v[i], sizeof(T) == 2 && bf16);
+    if (u % LANES < 4) s_scales[wave][u / LANES * 16 + 4 * (u & 3) + (lane >> 4)] = own.s;
+    // one wave's own LDS: its writes come before its reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    out[(uint64_t)tile * 64 + lane] = *reinterpret_cast<const u32x4*>(&s_words[wave][(lane >> 4) * 80 + u * 4]);
+    if (lane < GROUPS * 16) {
         const uint64_t at = (uint64_t)tile * (GROUPS * 16) + lane;
+        const float s = s_scales[wave][lane];
         if (bf16)
-            reinterpret_cast<__bf16*>(scales)[at] = (__bf16)mine;
+            reinterpret_cast<__bf16*>(scales)[at] = (__bf16)s;
         else
-            reinterpret_cast<float*>(scales)[at] = mine;
+            reinterpret_cast<float*>(scales)[at] = s;
     }
 }
 
