@@ -280,22 +280,25 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
     }
 }
 
+// Rounds of workgroups on the compute units times the work of one.
+uint64_t turns(const MatvecArgs& a, int wn) {
+    const uint64_t cus = (uint64_t)device_cu_count();
+    return (tiles_of(a.m, LAID_TOKENS) * tiles_of(a.nt, 4 * wn) + cus - 1) / cus * wn;
+}
+
 template <typename X, typename S, int GROUP>
 int launch_group(const MatvecArgs& a, hipStream_t s) {
-    // The widest workgroup of those that need the fewest turns of the compute
-    // units: rounds of workgroups times the work of one.
-    const uint64_t cus = (uint64_t)device_cu_count(), mblocks = tiles_of(a.m, LAID_TOKENS);
-    auto blocks = [&](int wn) { return mblocks * tiles_of(a.nt, 4 * wn); };
-    auto turns = [&](int wn) { return (blocks(wn) + cus - 1) / cus * wn; };
+    // The wider workgroup unless it needs more turns.
+    const uint64_t mblocks = tiles_of(a.m, LAID_TOKENS);
     auto go = [&](auto wn) -> int {
         constexpr int WN = decltype(wn)::value;
-        const uint64_t b = blocks(WN);
+        const uint64_t b = mblocks * tiles_of(a.nt, 4 * WN);
         if (b >= 1u << 31) return LECB_ERR_TOO_LARGE;
         matmul_w4_kernel<X, S, GROUP, WN>
             <<<dim3((uint32_t)(b + 7) / 8 * 8), 64 * MM_WAVES, 0, s>>>(a, (uint32_t)mblocks, (uint32_t)b);
         return launched();
     };
-    if (turns(8) <= turns(4)) return go(std::integral_constant<int, 8>());
+    if (turns(a, 8) <= turns(a, 4)) return go(std::integral_constant<int, 8>());
     return go(std::integral_constant<int, 4>());
 }
 
@@ -323,6 +326,11 @@ int lay_as(const MatvecArgs& a, uint32_t group, bool many, hipStream_t s) {
 }
 
 }  // namespace
+
+uint64_t matmul_w4_turns(const MatvecArgs& a) {
+    const uint64_t a8 = turns(a, 8), a4 = turns(a, 4);
+    return a8 < a4 ? a8 : a4;
+}
 
 int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s) {
     switch (x_type) {

@@ -390,7 +390,16 @@ int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s
     return scale_type == LECB_BF16 ? go(__bf16()) : go(float());
 }
 
-bool many(const MatvecArgs& a) { return a.m > 64 && a.kt < MM_TILES; }
+// Whether the form for many tokens takes it.  A round of its workgroups (64 x 256
+// outputs a compute unit) takes about 8/3 as long as one here (64 x 32):
+// 8192 x 8192 bf16, 65 to 128 tokens, 40 us here and 57 there; 300 tokens, 98 and
+// 60; 28672 x 4096, 48 tokens, 42 and 35; 1024 x 8192, 512 tokens, 26 and 60.
+bool many(const MatvecArgs& a) {
+    if (a.m <= 32 || a.kt >= MM_TILES) return false;
+    const uint64_t cus = (uint64_t)device_cu_count();
+    const uint64_t rounds = (tiles_of(a.m, 64) * tiles_of(a.nt, 2) + cus - 1) / cus;
+    return 3 * rounds > 2 * matmul_w4_turns(a);
+}
 
 }  // namespace
 
@@ -404,9 +413,10 @@ int launch_matvec_w4(const MatvecW4& m, void* stream) {
                        m.y_stride, m.n, m.k, m.m, (uint32_t)tiles_of(m.n, TILE_ROWS), (uint32_t)tiles_of(m.k, TILE_COLS),
                        m.xscale_stride, m.y_type};
     if (a.m > FEW_IN_ROWS) {
-        const int rc = launch_lay_tokens(a, m.x_type, m.group, many(a), s);
+        const bool are_many = many(a);
+        const int rc = launch_lay_tokens(a, m.x_type, m.group, are_many, s);
         if (rc) return rc;
-        if (many(a)) return launch_matmul_w4(a, m.x_type, m.scale_type, m.group, s);
+        if (are_many) return launch_matmul_w4(a, m.x_type, m.scale_type, m.group, s);
     }
     switch (m.x_type) {
         case LECB_I8: return launch_as<int8_t>(a, m.scale_type, m.group, s);
