@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
                         for (int i = 0; i < 2; ++i) acc[i] = O::mul32x2(xo[i][p], w0, w1, acc[i]);
                     }
                 }
-                const float s = (float)now->scales[wn][((2 * j + r / 16) * GROUPS + g) * 16 + r % 16];
+                const float s = (float)now->scales[wn][((2 * j + r / 16) * GROUPS + g) * 16 + r % 16] * O::SCALE;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -38,7 +38,7 @@ struct Sums {
         __device__ void spread() {
 #pragma unroll
             for (int q = 0; q < LOADS; ++q) {
-                const uint32_t v = __float_as_uint((float)raw[q]);
+                const uint32_t v = __float_as_uint((float)raw[q] * O::SCALE);
                 if constexpr (EACH == 1) {
                     scale[q] = __uint_as_float(v);
                 } else {

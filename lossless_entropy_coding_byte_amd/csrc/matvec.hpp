@@ -31,7 +31,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // and a packing take four times as long.  What is too much, 1.5 2^-8 times the
 // group's sum of x, is put into the sum beforehand: by an instruction whose
 // second operand is EXCESS, or from sums made before (Tokens).  2^-8 keeps the
-// sum over a group within the range of x.  FACTOR undoes 16 and 2^-8.
+// sum over a group within the range of x, exact for its smallest numbers too.
+// SCALE, of a group's scale, undoes 16 and 2^-8; FACTOR, of the result, 16.
 template <typename X>
 struct Operand;
 
@@ -45,7 +46,7 @@ template <>
 struct Operand<__bf16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float FACTOR = 4096.0f;
+    static constexpr float SCALE = 4096.0f, FACTOR = 1.0f;
     static constexpr bool OFFSET = true;
     static constexpr uint32_t EXCESS = 0xBBC0BBC0u;   // -1.5 2^-8, twice
     static __device__ A weights(uint32_t w) {
@@ -69,7 +70,7 @@ template <>
 struct Operand<_Float16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float FACTOR = 4096.0f;
+    static constexpr float SCALE = 4096.0f, FACTOR = 1.0f;
     static constexpr bool OFFSET = true;
     static constexpr uint32_t EXCESS = 0x9E009E00u;
     static __device__ A weights(uint32_t w) {
@@ -93,7 +94,7 @@ template <>
 struct Operand<int8_t> {
     typedef u32x2 A;
     typedef i32x4 Acc;
-    static constexpr float FACTOR = 0.0625f;
+    static constexpr float SCALE = 1.0f, FACTOR = 0.0625f;
     static constexpr bool OFFSET = false;
     static __device__ A weights(uint32_t w) { return {(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u}; }
     static __device__ u32x2 order(u32x2 x) {
