@@ -1,17 +1,21 @@
-"""Build liblecb.so (HIP kernels for gfx950 + host runtime) in-tree with hipcc.
+"""Build liblecb.so (HIP kernels for gfx950 + host runtime) in-tree with hipcc,
+and the Python module of the tensor functions with the host compiler.
 
 Run as ``python -m lossless_entropy_coding_byte_amd.build``; every call
-recompiles.  Output: ``lossless_entropy_coding_byte_amd/liblecb.so``.
+recompiles.  Output: ``lossless_entropy_coding_byte_amd/liblecb.so`` and, where
+torch is installed, ``lossless_entropy_coding_byte_amd/_tensors.so``.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +23,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblecb.so")
+TENSORS = os.path.join(PKG, "_tensors.so")   # the codec does without it, and without torch
 ARCH = "gfx950"
 
 SOURCES = ["kernels_misc.hip", "kernels_codebook.hip", "kernels_encode.hip", "kernels_decode.hip", "codebook.cpp",
@@ -80,10 +85,40 @@ def _compile(src: str, obj: str) -> tuple[str, int, str]:
     return src, rc, "\n".join(l for l in out.splitlines() if "remark:" not in l and not l.startswith("   "))
 
 
+def _run(cmd: list[str], what: str) -> None:
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + p.stdout + p.stderr)
+
+
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _compile_tensors(torch_dir: str, obj: str) -> None:
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    inc = [INCLUDE, f"{torch_dir}/include", f"{torch_dir}/include/torch/csrc/api/include", f"{rocm}/include",
+           sysconfig.get_paths()["include"]]
+    # torch's headers for this platform ask for these two names
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1"]
+         + [f"-I{i}" for i in inc] + ["-c", os.path.join(CSRC, "tensors.cpp"), "-o", obj], "compiling tensors.cpp")
+
+
+def _link_tensors(torch_dir: str, obj: str) -> None:
+    # torch's libraries are those the process already has; liblecb.so lies beside the module
+    _run(["g++", "-shared", "-o", TENSORS + ".tmp", obj, f"-L{torch_dir}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-lc10", "-lc10_hip", f"-L{PKG}", "-l:liblecb.so", "-Wl,-rpath,$ORIGIN"], "linking _tensors.so")
+    os.replace(TENSORS + ".tmp", TENSORS)
+
+
 def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(prefix="lecb_build_") as tmp:
         objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
         with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+            torch_dir = _torch_dir()
+            tensors = os.path.join(tmp, "tensors.o")
+            module = ex.submit(_compile_tensors, torch_dir, tensors) if torch_dir else None
             results = list(ex.map(_compile, SOURCES, objs))
         failed = False
         for src, rc, out in results:
@@ -99,6 +134,9 @@ def build(verbose: bool = False) -> str:
         if p.returncode != 0:
             raise RuntimeError("link failed:\n" + p.stdout + p.stderr)
         os.replace(tmp_lib, LIB)
+        if module:
+            module.result()
+            _link_tensors(torch_dir, tensors)
     return LIB
 
 

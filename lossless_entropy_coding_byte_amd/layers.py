@@ -4,7 +4,8 @@ and 8-bit activations that the codec stores, and what a layer computes with them
 ``lecb_*`` functions mirror the C ABI of ``include/lecb.h`` (explicit buffers,
 optional stream); the functions below them check shapes, types and devices
 (``ValueError``), allocate their results with torch and run on the current
-stream of the current device.  Every step runs in the HIP library.
+stream of the current device.  Every step runs in the HIP library; the functions
+that a layer calls step by step are native (``csrc/tensors.cpp``).
 
 >>> w4 = quantize_w4(weight)                             # [n, k] float -> 4-bit tiles + scales
 >>> q, scale, h = rmsnorm_q8(x, norm_weight, residual=r) # h = x + r; q int8, scale per row
@@ -15,13 +16,15 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, load
+from . import _check, _ptr, _stream, load
+
+load()   # raises if nothing is built
+from . import _tensors  # noqa: E402  (checks, results and calls of the tensor functions: csrc/tensors.cpp)
 
 LECB_F32, LECB_BF16, LECB_F16, LECB_I8 = 0, 1, 2, 3
 NORM_MAX_COLS = 32768
 
 _TYPES = {torch.float32: LECB_F32, torch.bfloat16: LECB_BF16, torch.float16: LECB_F16, torch.int8: LECB_I8}
-_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 _SCALES = (torch.float32, torch.bfloat16)
 
 
@@ -29,19 +32,6 @@ def _type(dtype, allowed, what):
     if dtype not in allowed:
         raise ValueError(f"{what}: {dtype} is not one of {', '.join(str(d) for d in allowed)}")
     return _TYPES[dtype]
-
-
-# A call on small tensors lasts as long as the host takes for it, so these two
-# are plain numbers, and the current stream is asked for by its handle: making
-# a Stream object of it takes 2.9 us, the handle 0.2 us.
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
-
-
-def _stream(stream=None):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # --------------------------------------------------------------------------- the C ABI, one to one
@@ -106,37 +96,6 @@ def _here(x, *tensors):
             raise ValueError(f"tensor on {t.device}: the current GPU's memory is needed")
 
 
-def _like(x, dtype):
-    """A new tensor of x's shape with rows side by side."""
-    # empty_like takes 1.2 us, new_empty 1.8; it keeps other orders of dimensions, which must not get here
-    return torch.empty_like(x, dtype=dtype) if x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
-
-
-def _rows_of(x, what):
-    """x as (rows, cols, row stride): any leading dimensions that are one stride apart, adjacent columns."""
-    if x.dim() == 0:
-        raise ValueError(f"{what}: at least one dimension is needed")
-    cols = x.shape[-1]
-    if x.is_contiguous():
-        return (x.numel() // cols if cols else 0), cols, cols
-    if cols > 1 and x.stride(-1) != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    rows = 1
-    stride = None
-    for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
-        if size == 1:
-            continue
-        if stride is None:
-            stride = st
-        elif st != stride * rows:
-            raise ValueError(f"{what}: rows must be one stride apart (strides {tuple(x.stride())})")
-        rows *= size
-    stride = cols if stride is None else stride
-    if stride < cols:
-        raise ValueError(f"{what}: rows overlap (strides {tuple(x.stride())})")
-    return rows, cols, stride
-
-
 class W4Weights:
     """4-bit weights [n, k] in the tile order of ``include/lecb.h``: ``tiles``
     (uint8, lecb_w4_tile_bytes) and ``scales`` (float32 or bfloat16,
@@ -158,28 +117,13 @@ class W4Weights:
 
 def quantize_w4(w, group: int = 128, scale_dtype=torch.bfloat16) -> W4Weights:
     """Round a float matrix [n, k] to 4-bit codes with one scale per row and ``group`` columns."""
-    if w.dim() != 2 or 0 in w.shape:
-        raise ValueError("quantize_w4: a matrix [n, k] is needed")
-    _type(w.dtype, _FLOATS, "quantize_w4")
-    _type(scale_dtype, _SCALES, "scale_dtype")
-    if group not in (32, 64, 128):
-        raise ValueError("quantize_w4: group is 32, 64 or 128")
-    n, k, stride = _rows_of(w, "quantize_w4")
-    _here(w)
-    nt, kt = -(-n // 16), -(-k // 128)
-    tiles = w.new_empty((nt, kt, 1024), dtype=torch.uint8)
-    scales = w.new_empty((nt, kt * (128 // group), 16), dtype=scale_dtype)
-    lecb_quantize_w4(w, stride, n, k, group, tiles, scales)
-    return W4Weights(tiles, scales, n, k, group)
+    tiles, scales = _tensors.quantize_w4(w, group, scale_dtype)
+    return W4Weights(tiles, scales, *w.shape, group)
 
 
 def dequantize_w4(w4: W4Weights, dtype=torch.bfloat16):
     """The weights [n, k] that the codes stand for."""
-    _type(dtype, _FLOATS, "dequantize_w4")
-    _here(w4.tiles, w4.scales)
-    out = w4.tiles.new_empty((w4.n, w4.k), dtype=dtype)
-    lecb_dequantize_w4(w4.tiles, w4.scales, w4.group, w4.n, w4.k, out, w4.k)
-    return out
+    return _tensors.dequantize_w4(w4.tiles, w4.scales, w4.group, w4.n, w4.k, dtype)
 
 
 def tile_w4(rows, n: int, k: int):
@@ -211,49 +155,12 @@ def rmsnorm_q8(x, weight, residual=None, eps: float = 1e-6, scale=None, out_h=No
     x itself.  scale: a float32 tensor of one number fixes the scale for every
     row (values past it saturate) and is returned as given.  out_h: where h
     goes; x or residual themselves will do."""
-    rows, cols, xs = _rows_of(x, "rmsnorm_q8")
-    _type(x.dtype, _FLOATS, "rmsnorm_q8")
-    _type(weight.dtype, _FLOATS, "rmsnorm_q8: weight")
-    if not 1 <= cols <= NORM_MAX_COLS:
-        raise ValueError(f"rmsnorm_q8: rows have 1 to {NORM_MAX_COLS} columns")
-    if weight.numel() != cols or not weight.is_contiguous():
-        raise ValueError("rmsnorm_q8: weight holds one contiguous number per column")
-    _here(x, weight, residual, scale, out_h)
-    rs, h, hs = 0, None, 0
-    if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
-            raise ValueError("rmsnorm_q8: residual has x's shape and type")
-        _, _, rs = _rows_of(residual, "rmsnorm_q8: residual")
-        h = out_h if out_h is not None else _like(x, x.dtype)
-        if h.shape != x.shape or h.dtype != x.dtype:
-            raise ValueError("rmsnorm_q8: out_h has x's shape and type")
-        _, _, hs = _rows_of(h, "rmsnorm_q8: out_h")
-    elif out_h is not None:
-        raise ValueError("rmsnorm_q8: without a residual h is x")
-    if scale is None:
-        s = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    else:
-        s = scale
-        if s.dtype != torch.float32 or s.numel() != 1:
-            raise ValueError("rmsnorm_q8: a fixed scale is one float32 number")
-    q = _like(x, torch.int8)
-    lecb_rmsnorm_q8(x, xs, residual, rs, weight, rows, cols, eps, h, hs, q, s, scale is not None)
-    return q, s, (x if h is None else h)
+    return _tensors.rmsnorm_q8(x, weight, residual, eps, scale, out_h)
 
 
 def dequantize_q8(q, scale, dtype=torch.bfloat16):
     """The values q * scale of int8 codes [..., cols]; scale: one float32 per row, or one."""
-    _type(dtype, _FLOATS, "dequantize_q8")
-    if q.dtype != torch.int8 or not q.is_contiguous() or q.dim() == 0:
-        raise ValueError("dequantize_q8: contiguous int8 codes are needed")
-    cols = q.shape[-1]
-    rows = q.numel() // cols if cols else 0
-    if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() not in (1, rows):
-        raise ValueError("dequantize_q8: one float32 scale per row, or one")
-    _here(q, scale)
-    out = _like(q, dtype)
-    lecb_dequantize_q8(q, rows, cols, scale, int(scale.numel() != 1), out)
-    return out
+    return _tensors.dequantize_q8(q, scale, dtype)
 
 
 def matvec_w4(x, w4: W4Weights, x_scale=None, out_dtype=None, ws=None):
@@ -262,23 +169,4 @@ def matvec_w4(x, w4: W4Weights, x_scale=None, out_dtype=None, ws=None):
     Returns y [..., n] of out_dtype (x's type; bfloat16 for int8 x).  ws: a
     uint8 workspace of lecb_matvec_w4_workspace_bytes that the caller keeps;
     calls that overlap in time must not share one."""
-    m, k, xs = _rows_of(x, "matvec_w4")
-    if k != w4.k:
-        raise ValueError(f"matvec_w4: x has {k} columns, the weights {w4.k}")
-    is_int = x.dtype == torch.int8
-    if not is_int:
-        _type(x.dtype, (torch.int8, torch.bfloat16, torch.float16), "matvec_w4")
-    step = 0
-    if x_scale is not None:
-        if not is_int or x_scale.dtype != torch.float32 or not x_scale.is_contiguous() or x_scale.numel() not in (1, m):
-            raise ValueError("matvec_w4: x_scale goes with int8 x, one float32 per row or one")
-        step = int(x_scale.numel() != 1)
-    dtype = out_dtype if out_dtype is not None else torch.bfloat16 if is_int else x.dtype
-    _type(dtype, _FLOATS, "matvec_w4: out_dtype")
-    _here(x, w4.tiles, w4.scales, x_scale, ws)
-    y = x.new_empty((*x.shape[:-1], w4.n), dtype=dtype)
-    if ws is None:
-        need = lecb_matvec_w4_workspace_bytes(m, w4.n, w4.k)
-        ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    lecb_matvec_w4(x, xs, x_scale, step, m, w4.tiles, w4.scales, w4.group, w4.n, w4.k, y, w4.n, ws)
-    return y
+    return _tensors.matvec_w4(x, w4.tiles, w4.scales, w4.n, w4.k, w4.group, x_scale, out_dtype, ws)
