@@ -303,7 +303,20 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_q8_kernel(NormArgs a) {
     T* h = a.h ? reinterpret_cast<T*>(a.h) + row * a.h_stride : nullptr;
     const W* weight = reinterpret_cast<const W*>(a.weight);
     int8_t* q = a.q + row * cols;
+    // everything is asked for before anything is used: a row is as long as one
+    // lane's loads take, and h may be where x or the residual is
     float v[NV][8];
+    Piece<T> bx[NV], br[NV];
+    Piece<W> bw[NV];
+#pragma unroll
+    for (int p = 0; p < NV; ++p) {
+        const uint32_t c = c0 + p * THREADS * 8;
+        if (c < cols) {
+            bx[p].load(x + c, cols - c);
+            if (res) br[p].load(res + c, cols - c);
+            bw[p].load(weight + c, cols - c);
+        }
+    }
     RowSums<THREADS> sums{0.0f, 0u};
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
@@ -311,27 +324,23 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_q8_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
         if (c < cols) {
-            Piece<T> b;
-            b.load(x + c, cols - c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = b[i];
+            for (int i = 0; i < 8; ++i) v[p][i] = bx[p][i];
             if (res) {
-                b.load(res + c, cols - c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] += b[i];
+                for (int i = 0; i < 8; ++i) v[p][i] += br[p][i];
             }
             if (h) {
+                Piece<T> b;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) b.set(i, v[p][i]);
                 b.store(h + c, cols - c);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sums.ss = fmaf(v[p][i], v[p][i], sums.ss);
-            Piece<W> w;
-            w.load(weight + c, cols - c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[p][i] *= w[i];   // from here on v = h weight
+                v[p][i] *= bw[p][i];   // from here on v = h weight
                 sums.amax = umax(sums.amax, abs_bits(v[p][i]));
             }
         }
