@@ -86,7 +86,9 @@ struct Step {
             }
         }
         q ^= 0x88888888u;
-        if (!(worst + worst < s && s >= 0x1p-60f && s < 0x1p100f)) {
+        if (s == 0.0f) {   // padding, for the most part
+            q = 0;
+        } else if (!(worst + worst < s && s >= 0x1p-60f && s < 0x1p100f)) {
             q = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) q |= code(w[i]) << (4 * i);
@@ -382,16 +384,24 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_q8_kernel(NormArgs a) {
     }
 }
 
-// A lane turns 16 neighbouring codes into values; a piece may span rows.
+// A lane turns 16 neighbouring codes into values.  They may span rows: two at
+// most, whose scales are asked for at once, where rows have 16 columns or more.
 template <typename T>
 __global__ __launch_bounds__(256) void dequantize_q8_kernel(const int8_t* __restrict__ q, uint64_t total,
                                                             uint32_t cols, const float* __restrict__ scale,
                                                             int scale_stride, T* __restrict__ out) {
     const uint64_t at = ((uint64_t)blockIdx.x * 256 + threadIdx.x) * 16;
     if (at >= total) return;
-    uint64_t row = scale_stride ? at / cols : 0;
-    uint32_t col = scale_stride ? (uint32_t)(at - row * cols) : 0;
-    float s = scale[row];
+    uint64_t row = 0;
+    uint32_t left = 16;   // codes of this row
+    float s[2] = {scale[0], 0.0f};
+    if (scale_stride) {
+        // a quotient of 64 bits takes several times as long as one of 32
+        row = total <= 0xffffffffu ? (uint32_t)at / cols : at / cols;
+        left = (uint32_t)((row + 1) * cols - at);
+        s[0] = scale[row];
+        s[1] = scale[row + (at + left < total)];
+    }
     const bool whole = at + 16 <= total;
     u32x4 b = {0, 0, 0, 0};
     if (whole) {
@@ -400,12 +410,19 @@ __global__ __launch_bounds__(256) void dequantize_q8_kernel(const int8_t* __rest
         for (uint32_t i = 0; at + i < total; ++i) b[i / 4] |= (uint32_t)(uint8_t)q[at + i] << (8 * (i % 4));
     }
     Piece<T> v[2];
+    if (cols >= 16 || !scale_stride) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i / 8].set(i % 8, product((float)((int)(b[i / 4] << (24 - 8 * (i % 4))) >> 24), s));
-        if (scale_stride && ++col == cols && at + i + 1 < total) {
-            col = 0;
-            s = scale[++row];
+        for (int i = 0; i < 16; ++i)
+            v[i / 8].set(i % 8, product((float)((int)(b[i / 4] << (24 - 8 * (i % 4))) >> 24), (uint32_t)i < left ? s[0] : s[1]));
+    } else {
+        float f = s[0];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i / 8].set(i % 8, product((float)((int)(b[i / 4] << (24 - 8 * (i % 4))) >> 24), f));
+            if (--left == 0 && at + i + 1 < total) {
+                left = cols;
+                f = scale[++row];
+            }
         }
     }
     v[0].store(out + at, total - at);

@@ -119,12 +119,17 @@ struct Piece {
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = *reinterpret_cast<const loose*>(p + j * PER);
     }
-    __device__ void load(const T* p, uint64_t count) {   // zeros past `count`
+    // zeros past `count`; entries past it repeat the last one's load (p[0] where
+    // there is none: it has to be readable), so that all are in flight at once
+    __device__ void load(const T* p, uint64_t count) {
         if (count >= 8) {
             load(p);
         } else {
+            T e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i / PER][i % PER] = (uint64_t)i < count ? p[i] : (T)0.0f;
+            for (int i = 0; i < 8; ++i) e[i] = p[(uint64_t)i < count ? i : count ? count - 1 : 0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i / PER][i % PER] = (uint64_t)i < count ? e[i] : (T)0.0f;
         }
     }
     __device__ float operator[](int i) const { return (float)v[i / PER][i % PER]; }
