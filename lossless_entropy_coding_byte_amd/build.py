@@ -108,7 +108,7 @@ def _compile_tensors(torch_dir: str, obj: str) -> None:
 def _link_tensors(torch_dir: str, obj: str) -> None:
     # torch's libraries are those the process already has; liblecb.so lies beside the module
     _run(["g++", "-shared", "-o", TENSORS + ".tmp", obj, f"-L{torch_dir}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
-          "-lc10", "-lc10_hip", f"-L{PKG}", "-l:liblecb.so", "-Wl,-rpath,$ORIGIN"], "linking _tensors.so")
+          "-ltorch_hip", "-lc10", "-lc10_hip", f"-L{PKG}", "-l:liblecb.so", "-Wl,-rpath,$ORIGIN"], "linking _tensors.so")
     os.replace(TENSORS + ".tmp", TENSORS)
 
 

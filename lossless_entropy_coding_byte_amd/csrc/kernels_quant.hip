@@ -112,6 +112,11 @@ __device__ inline float of_quad(float v) {   // lane I's of each four
 // neighbouring lanes.  Lane i of each four makes the step of load i's row, as the
 // two divisions cost as much as four weights' codes.  The words go through LDS
 // into the tile's order, so that it leaves in one store.
+//
+// Bound by HBM, with the vector instructions (about 9 a weight) close behind:
+// 8192 x 8192 bf16, groups of 128, 39 us, 4.3 TB/s; fp32, groups of 64, 64 us,
+// 4.7 TB/s (a large copy: 5.0).  By 64-byte pieces of 16 rows, as the tile lies,
+// the loads and fourteen instructions a weight took 46 and 72 us.
 template <typename T, int GROUP>
 __global__ __launch_bounds__(256) void quantize_w4_kernel(const T* __restrict__ w, uint64_t stride, uint64_t n,
                                                           uint64_t k, uint32_t kt, uint32_t tiles,
@@ -168,28 +173,38 @@ __global__ __launch_bounds__(256) void quantize_w4_kernel(const T* __restrict__ 
 
 __device__ inline float code_value(uint32_t word, int i) { return (float)((int)(word << (28 - 4 * i)) >> 28); }
 
-template <typename T>
+// A wave a tile; its words go through LDS to lanes that write four whole rows'
+// columns at a time, as in quantize_w4_kernel.  Bound by the writes.
+template <typename T, int GROUP>
 __global__ __launch_bounds__(256) void dequantize_w4_kernel(const u32x4* __restrict__ in,
-                                                            const void* __restrict__ scales, int bf16,
-                                                            uint32_t group, uint64_t n, uint64_t k, uint32_t kt,
-                                                            uint32_t tiles, T* __restrict__ out, uint64_t stride) {
-    const uint32_t tile = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                                            const void* __restrict__ scales, int bf16, uint64_t n,
+                                                            uint64_t k, uint32_t kt, uint32_t tiles,
+                                                            T* __restrict__ out, uint64_t stride) {
+    constexpr int GROUPS = 128 / GROUP, LANES = GROUP / 8;
+    __shared__ __attribute__((aligned(16))) uint32_t s_words[4][4 * 80];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile = blockIdx.x * 4 + wave;
     if (tile >= tiles) return;
-    const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
-    const uint64_t row = (uint64_t)(tile / kt) * TILE_ROWS + r;
-    const uint64_t col = (uint64_t)(tile % kt) * TILE_COLS + 8 * c;
-    const u32x4 words = in[(uint64_t)tile * 64 + lane];
-    if (row >= n || col >= k) return;
-    T* p = out + row * stride + col;
+    const uint32_t lane = threadIdx.x & 63, u = lane & 15;
+    *reinterpret_cast<u32x4*>(&s_words[wave][(lane >> 4) * 80 + u * 4]) = in[(uint64_t)tile * 64 + lane];
+    float s[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint64_t at = ((uint64_t)tile * (TILE_COLS / group) + 32 * d / group) * 16 + r;
-        const float s = bf16 ? (float)reinterpret_cast<const __bf16*>(scales)[at]
-                             : reinterpret_cast<const float*>(scales)[at];
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t at = ((uint64_t)tile * GROUPS + u / LANES) * 16 + 4 * i + (lane >> 4);
+        s[i] = bf16 ? (float)reinterpret_cast<const __bf16*>(scales)[at] : reinterpret_cast<const float*>(scales)[at];
+    }
+    // one wave's own LDS: its write comes before its reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    const uint64_t col = (uint64_t)(tile % kt) * TILE_COLS + 8 * u;
+    if (col >= k) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = 4 * i + (lane >> 4);
+        const uint64_t row = (uint64_t)(tile / kt) * TILE_ROWS + r;
+        const uint32_t word = s_words[wave][(u & 3) * 80 + r * 4 + (u >> 2)];
         Piece<T> v;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.set(i, product(code_value(words[d], i), s));
-        if (col + 32 * d < k) v.store(p + 32 * d, k - col - 32 * d);
+        for (int e = 0; e < 8; ++e) v.set(e, product(code_value(word, e), s[i]));
+        if (row < n) v.store(out + row * stride + col, k - col);
     }
 }
 
@@ -251,7 +266,11 @@ __global__ __launch_bounds__(256) void untile_w4_kernel(const u32x4* __restrict_
 // eight elements a lane).  With a = max|h weight|, the scale is a r / 127 for
 // r = 1 / sqrt(mean(h^2) + eps) and the codes are rint(h weight 127 / a): r
 // cancels, so the sum of squares and the maximum come out of one pass and one
-// reduction.
+// reduction.  The order of the sums depends on the number of columns alone.
+//
+// Bound by HBM: 16384 x 2048 bf16 with the residual 40 us, 5.9 TB/s of what it
+// reads and writes; 4096 x 8192 fp32 86 us, 5.0 TB/s; one row of 4096 takes
+// 3.4 us, two memory latencies and the reduction.
 template <int THREADS>
 struct RowSums {
     float ss;
@@ -386,6 +405,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_q8_kernel(NormArgs a) {
 
 // A lane turns 16 neighbouring codes into values.  They may span rows: two at
 // most, whose scales are asked for at once, where rows have 16 columns or more.
+// Bound by HBM: 16384 x 2048 to bf16 in 19 us, 5.3 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void dequantize_q8_kernel(const int8_t* __restrict__ q, uint64_t total,
                                                             uint32_t cols, const float* __restrict__ scale,
@@ -476,9 +496,17 @@ int launch_dequantize_w4(const DequantizeW4& a, void* stream) {
     const dim3 grid((uint32_t)((tiles + 3) / 4));
     return with_float_type(a.type, [&](auto t) -> int {
         typedef decltype(t) T;
-        dequantize_w4_kernel<T><<<grid, 256, 0, s>>>(reinterpret_cast<const u32x4*>(a.tiles), a.scales, a.scale_type == LECB_BF16,
-                                    a.group, a.n, a.k, (uint32_t)kt, (uint32_t)tiles, static_cast<T*>(a.out),
-                                    a.stride);
+        auto go = [&](auto group) {
+            dequantize_w4_kernel<T, decltype(group)::value><<<grid, 256, 0, s>>>(
+                reinterpret_cast<const u32x4*>(a.tiles), a.scales, a.scale_type == LECB_BF16, a.n, a.k, (uint32_t)kt,
+                (uint32_t)tiles, static_cast<T*>(a.out), a.stride);
+        };
+        if (a.group == 32)
+            go(std::integral_constant<int, 32>());
+        else if (a.group == 64)
+            go(std::integral_constant<int, 64>());
+        else
+            go(std::integral_constant<int, 128>());
         return launched();
     });
 }

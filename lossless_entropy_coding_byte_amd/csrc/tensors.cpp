@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -108,7 +109,8 @@ struct Rows {
 };
 
 at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) {
-    return at::empty(size, at::TensorOptions().dtype(t).device(like.device()));
+    // what at::empty comes to on a GPU, without its dispatch
+    return at::Tensor(at::detail::empty_cuda(size, t, like.device(), std::nullopt));
 }
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 void done(int status, const char* where) {
