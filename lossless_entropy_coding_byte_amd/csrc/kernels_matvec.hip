@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
     typedef Operand<X> O;
     typedef Tokens<X> T;
     typedef Sums<X, S, GROUP, MT, NT> Su;
-    static_assert(ROWS == 0 || MT == 1, "tokens in rows: 8 at most");
+    static_assert(ROWS == 0 || MT == 1, "tokens in rows: 16 at most");
     constexpr int COLS = 16 * NT, PITCH = COLS + 4;   // outputs of a token; + 4: rows on other banks
     constexpr int TOKENS = ROWS ? ROWS : 16 * MT;
     __shared__ float part[few_waves(MT, NT)][TOKENS][PITCH];
@@ -364,36 +364,51 @@ int launch_few(const MatvecArgs& a, hipStream_t s) {
 }
 
 template <typename X, typename S, int GROUP>
-int launch_group(const MatvecArgs& a, hipStream_t s) {
+int launch_group(const MatvecArgs& a, bool rows, hipStream_t s) {
     // More rows of W for a wave spare loads of x, fewer make more workgroups:
     // as many as leave one workgroup per compute unit.
     const uint32_t cus = (uint32_t)device_cu_count();
     auto go = [&](auto mt, auto in_rows) -> int {
         constexpr int MT = decltype(mt)::value, ROWS = decltype(in_rows)::value;
-        const uint64_t rows = a.nt * tiles_of(a.m, 16 * MT);
+        const uint64_t blocks = a.nt * tiles_of(a.m, 16 * MT);
         if constexpr (MT < 4) {
-            if (rows >= 4 * cus) return launch_few<X, S, GROUP, MT, 4, ROWS>(a, s);
+            if (blocks >= 4 * cus) return launch_few<X, S, GROUP, MT, 4, ROWS>(a, s);
         }
-        if (rows >= 2 * cus) return launch_few<X, S, GROUP, MT, 2, ROWS>(a, s);
+        if (blocks >= 2 * cus) return launch_few<X, S, GROUP, MT, 2, ROWS>(a, s);
         return launch_few<X, S, GROUP, MT, 1, ROWS>(a, s);
     };
     typedef std::integral_constant<int, 0> Laid;
-    if (a.m <= 4) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
-    if (a.m <= FEW_IN_ROWS) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
-    if (a.m <= 16) return go(std::integral_constant<int, 1>(), Laid());
+    typedef std::integral_constant<int, 1> One;
+    if (rows && a.m <= 4) return go(One(), std::integral_constant<int, 4>());
+    if (rows && a.m <= 8) return go(One(), std::integral_constant<int, 8>());
+    if (rows) return go(One(), std::integral_constant<int, 16>());
+    if (a.m <= 16) return go(One(), Laid());
     if (a.m <= 32) return go(std::integral_constant<int, 2>(), Laid());
     return go(std::integral_constant<int, 4>(), Laid());
 }
 
 template <typename X>
-int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s) {
+int launch_as(const MatvecArgs& a, bool rows, int scale_type, uint32_t group, hipStream_t s) {
     auto go = [&](auto scale) -> int {
         typedef decltype(scale) S;
-        if (group == 32) return launch_group<X, S, 32>(a, s);
-        if (group == 64) return launch_group<X, S, 64>(a, s);
-        return launch_group<X, S, 128>(a, s);
+        if (group == 32) return launch_group<X, S, 32>(a, rows, s);
+        if (group == 64) return launch_group<X, S, 64>(a, rows, s);
+        return launch_group<X, S, 128>(a, rows, s);
     };
     return scale_type == LECB_BF16 ? go(__bf16()) : go(float());
+}
+
+// Whether tokens are read from their rows, without a launch to lay them out
+// first (2.6 us, and as much of the host: 5 x 1003 x 1111 takes 9.6 us so, 5.5 in
+// rows): always up to four, and up to 16 where rows are short; up to 16 too where
+// their loads are aligned and, above eight, rows not too long.  8192 x 8192 bf16,
+// in rows and laid out, us: 8 tokens 10.2 and 13.5, 16 tokens 14 and 13.7; 8
+// tokens of 8191 columns 19.3 and 13.4; 1000 x 28672, 16 tokens, 34 and 25.  Both
+// give the same bits: the same instructions on the same operands, in the same order.
+bool in_rows(const MatvecArgs& a, uint64_t bytes) {
+    if (a.m <= 4 || (a.m <= 16 && a.kt <= 16)) return true;
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.x) | a.x_stride * bytes) % (8 * bytes) == 0;
+    return aligned && (a.m <= 8 || (a.m <= 16 && a.kt <= 64));
 }
 
 // Whether the form for many tokens takes it.  A round of its workgroups (64 x 256
@@ -410,7 +425,8 @@ bool many(const MatvecArgs& a) {
 }  // namespace
 
 uint64_t matvec_w4_workspace(uint64_t m, uint64_t, uint64_t k) {
-    return m <= FEW_IN_ROWS ? 0 : laid_bytes(m, tiles_of(k, TILE_COLS));
+    const uint64_t kt = tiles_of(k, TILE_COLS);
+    return m <= 4 || (m <= 8 && kt <= 16) ? 0 : laid_bytes(m, kt);   // what no address needs is not asked for
 }
 
 int launch_matvec_w4(const MatvecW4& m, void* stream) {
@@ -418,16 +434,17 @@ int launch_matvec_w4(const MatvecW4& m, void* stream) {
     const MatvecArgs a{m.x, m.xscale, reinterpret_cast<const u32x4*>(m.tiles), m.scales, m.y, m.ws, m.x_stride,
                        m.y_stride, m.n, m.k, m.m, (uint32_t)tiles_of(m.n, TILE_ROWS), (uint32_t)tiles_of(m.k, TILE_COLS),
                        m.xscale_stride, m.y_type};
-    if (a.m > FEW_IN_ROWS) {
+    const bool rows = in_rows(a, elem_bytes(m.x_type));
+    if (!rows) {
         const bool are_many = many(a);
         const int rc = launch_lay_tokens(a, m.x_type, m.group, are_many, s);
         if (rc) return rc;
         if (are_many) return launch_matmul_w4(a, m.x_type, m.scale_type, m.group, s);
     }
     switch (m.x_type) {
-        case LECB_I8: return launch_as<int8_t>(a, m.scale_type, m.group, s);
-        case LECB_BF16: return launch_as<__bf16>(a, m.scale_type, m.group, s);
-        default: return launch_as<_Float16>(a, m.scale_type, m.group, s);
+        case LECB_I8: return launch_as<int8_t>(a, rows, m.scale_type, m.group, s);
+        case LECB_BF16: return launch_as<__bf16>(a, rows, m.scale_type, m.group, s);
+        default: return launch_as<_Float16>(a, rows, m.scale_type, m.group, s);
     }
 }
 

@@ -256,8 +256,6 @@ __device__ inline float* laid_sums(const MatvecArgs& a) {
     return reinterpret_cast<float*>(reinterpret_cast<u32x4*>(a.ws) + laid_units(a.m, a.kt, sizeof(X)));
 }
 
-constexpr uint64_t FEW_IN_ROWS = 8;   // tokens that are read from their rows
-
 int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s);
 constexpr uint32_t MM_TILES = 1u << 22;   // more tiles of columns than this: in the form for few tokens
 uint64_t matmul_w4_turns(const MatvecArgs& a);   // its time, in 64 x 64 outputs of a wave

@@ -1,7 +1,7 @@
 // The operators of quantised layers on torch tensors: checks, results from
 // torch's allocator, one call of the C ABI each.  layers.py documents them and
 // is what users call.  On small tensors a call lasts as long as the host takes:
-// rmsnorm_q8 of one row 6 us here, 13 us with the same steps in Python and ctypes.
+// rmsnorm_q8 of one row 4.8 us here, 13 us with the same steps in Python and ctypes.
 #include <Python.h>
 
 #include <ATen/ATen.h>

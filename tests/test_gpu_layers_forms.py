@@ -123,6 +123,25 @@ def test_quantize_halves_of_steps(dtype, sdt, group):
     assert torch.equal(w4.tiles.cpu(), ref_tiles(q))
 
 
+@pytest.mark.parametrize("m", [1, 4, 5, 8, 9, 13, 16])
+@pytest.mark.parametrize("k", [1160, 1111, 8320])
+@pytest.mark.parametrize("dtype", [I8, BF16, F16], ids=str)
+def test_few_tokens_by_alignment(m, k, dtype):
+    """Aligned rows are read as they lie, others laid out first: the same bits, whatever the address and stride."""
+    n = 300
+    q, s, w4 = weights(n, k, 64, BF16, m + k)
+    x, _ = tokens(m, k, dtype, m * k)
+    ref = None
+    for pad, start in ((0, 0), (8, 0), (8, 8), (16, 16), (3, 0), (9, 1)):
+        big = torch.zeros(m, (k + 15) // 16 * 16 + pad, dtype=dtype, device=DEV)
+        big[:, start : start + k] = x.to(DEV)
+        y = lecb.matvec_w4(big[:, start : start + k], w4, out_dtype=F32)
+        if ref is None:
+            ref = y
+            check_matvec(y, x, None, q, s, 64)
+        assert torch.equal(y, ref), (pad, start)
+
+
 def test_workspace_of_the_caller():
     """A workspace kept by the caller, its contents of no matter; calls with less are refused."""
     q, s, w4 = weights(80, 512, 64, BF16, 11)
