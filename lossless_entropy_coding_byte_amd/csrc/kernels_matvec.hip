@@ -135,13 +135,13 @@ struct Sums {
     }
 };
 
-// A wave's tiles, every `waves`-th from `wave` on: fetch(d, tile) for DEPTH of
-// them ahead of add(d).  Past its last tile a wave fetches that one again.
+// A wave's tiles, every `waves`-th from `first` to `end`: fetch(d, tile) for DEPTH
+// of them ahead of add(d).  Past its last tile a wave fetches that one again.
 template <int DEPTH, typename Fetch, typename Add>
-__device__ __forceinline__ void run(uint32_t wave, uint32_t waves, uint32_t tiles, Fetch fetch, Add add) {
-    if (wave >= tiles) return;
-    const uint32_t mine = (tiles - wave + waves - 1) / waves;
-    auto tile = [&](uint32_t t) { return wave + (t < mine ? t : mine - 1) * waves; };
+__device__ __forceinline__ void run(uint32_t first, uint32_t waves, uint32_t end, Fetch fetch, Add add) {
+    if (first >= end) return;
+    const uint32_t mine = (end - first + waves - 1) / waves;
+    auto tile = [&](uint32_t t) { return first + (t < mine ? t : mine - 1) * waves; };
     uint32_t t = 0;
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) fetch(d, tile(d));
@@ -214,7 +214,9 @@ struct InRows {
 // times ROWS tokens in their rows.  Its waves share the columns out, tile by
 // tile, each with the next tiles' loads in flight while it works on one, and
 // add their sums up in LDS in a fixed order.  (64 tokens' tiles are too large
-// for that: their words are one tile ahead, tokens half of one.)
+// for that: their words are one tile ahead, tokens half of one.)  Where there are
+// few rows of W and many columns, several workgroups share the columns of a block
+// (blockIdx.z); add_parts_kernel adds their sums up.
 //
 // One token: bound by HBM where W is large (28672 x 8192 bf16 25 us, 4.8 TB/s; W
 // is read once and does not stay in the cache) and by latency where it is not
@@ -233,6 +235,8 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
     const uint32_t waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
     const uint32_t n0 = blockIdx.x * NT, mt0 = blockIdx.y * MT;
+    const uint32_t share = (a.kt + a.splits - 1) / a.splits, from = blockIdx.z * share;
+    const uint32_t until = from + share < a.kt ? from + share : a.kt;   // tiles of this workgroup (none: zeros)
     // tiles past the last repeat it: their sums are not stored
     auto tile_row = [&](uint32_t j) -> uint64_t { return n0 + j < a.nt ? n0 + j : a.nt - 1; };
     const u32x4* tiles[NT];
@@ -264,13 +268,13 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
             sums.template add<1>(ww, h);
         };
         run<DEPTH>(
-            wave, waves, whole,
+            from + wave, waves, until < whole ? until : whole,
             [&](int d, uint32_t tk) {
                 x[d].load(row + (uint64_t)tk * TILE_COLS, r, c);
                 w[d].load(tiles, scales, tk, lane);
             },
             [&](int d) { add(w[d], x[d]); });
-        if (whole < a.kt && wave == whole % waves) {   // the columns that do not fill a tile
+        if (whole < until && from <= whole && wave == (whole - from) % waves) {   // the columns that do not fill a tile
             x[0].load(row + (uint64_t)whole * TILE_COLS, r, c, (uint32_t)(a.k % TILE_COLS));
             w[0].load(tiles, scales, whole, lane);
             add(w[0], x[0]);
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
             typename Su::Weights w[DEPTH];
             typename Su::Half h[DEPTH][2];
             run<DEPTH>(
-                wave, waves, a.kt,
+                from + wave, waves, until,
                 [&](int d, uint32_t tk) {
                     load(h[d][0], tk, 0);
                     load(h[d][1], tk, 1);
@@ -307,25 +311,25 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
         } else {
             typename Su::Weights w0, w1;
             typename Su::Half h0, h1;
-            uint32_t tk = wave;
-            if (tk < a.kt) {
+            uint32_t tk = from + wave;
+            if (tk < until) {
                 load(h0, tk, 0);
                 w0.load(tiles, scales, tk, lane);
             }
-            while (tk < a.kt) {
+            while (tk < until) {
                 const uint32_t t1 = tk + waves, t2 = t1 + waves;
                 load(h1, tk, 1);
-                if (t1 < a.kt) w1.load(tiles, scales, t1, lane);
+                if (t1 < until) w1.load(tiles, scales, t1, lane);
                 w0.spread();
                 sums.template add<0>(w0, h0);
-                if (t1 < a.kt) load(h0, t1, 0);
+                if (t1 < until) load(h0, t1, 0);
                 sums.template add<1>(w0, h1);
-                if (t1 >= a.kt) break;
+                if (t1 >= until) break;
                 load(h1, t1, 1);
-                if (t2 < a.kt) w0.load(tiles, scales, t2, lane);
+                if (t2 < until) w0.load(tiles, scales, t2, lane);
                 w1.spread();
                 sums.template add<0>(w1, h0);
-                if (t2 < a.kt) load(h0, t2, 0);
+                if (t2 < until) load(h0, t2, 0);
                 sums.template add<1>(w1, h1);
                 tk = t2;
             }
@@ -346,8 +350,24 @@ __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(Matve
         if (token >= a.m || col >= a.n) continue;
         f32x4 v = *reinterpret_cast<const f32x4*>(&part[0][t][n]);
         for (uint32_t w = 1; w < waves; ++w) v += *reinterpret_cast<const f32x4*>(&part[w][t][n]);
-        store_y(a, token, col, v * O::FACTOR);
+        v *= O::FACTOR;
+        if (a.splits > 1)
+            *reinterpret_cast<f32x4*>(a.parts + (blockIdx.z * a.m + token) * (16 * (uint64_t)a.nt) + col) = v;
+        else
+            store_y(a, token, col, v);
     }
+}
+
+// The shares' sums, four outputs a lane, in the order of the columns.
+__global__ __launch_bounds__(64) void add_parts_kernel(MatvecArgs a) {
+    const uint64_t at = (uint64_t)blockIdx.x * 64 + threadIdx.x, row = 4 * (uint64_t)a.nt;   // fours of a token
+    if (at >= a.m * row) return;
+    const uint64_t token = at / row, col = at % row * 4;
+    if (col >= a.n) return;
+    f32x4 v = {0, 0, 0, 0};
+    for (uint32_t z = 0; z < a.splits; ++z)
+        v += *reinterpret_cast<const f32x4*>(a.parts + ((z * a.m + token) * row * 4 + col));
+    store_y(a, token, col, v);
 }
 
 template <typename X, typename S, int GROUP, int MT, int NT, int ROWS>
@@ -357,9 +377,11 @@ int launch_few(const MatvecArgs& a, hipStream_t s) {
     // No more waves than have DEPTH tiles each, but four: what a wave asks for past
     // its last tile costs loads, a wave more only a share of the last sums.
     uint32_t waves = few_waves(MT, NT);
-    while (waves > 4 && waves * few_depth(MT, NT) > a.kt) waves /= 2;
+    while (waves > 4 && waves * few_depth(MT, NT) > tiles_of(a.kt, a.splits)) waves /= 2;
     matvec_w4_kernel<X, S, GROUP, MT, NT, ROWS>
-        <<<dim3((uint32_t)tiles_of(a.nt, NT), (uint32_t)mt), waves * 64, 0, s>>>(a);
+        <<<dim3((uint32_t)tiles_of(a.nt, NT), (uint32_t)mt, a.splits), waves * 64, 0, s>>>(a);
+    if (a.splits > 1)
+        add_parts_kernel<<<dim3((uint32_t)tiles_of(a.m * a.nt, 16)), 64, 0, s>>>(a);
     return launched();
 }
 
@@ -411,6 +433,21 @@ bool in_rows(const MatvecArgs& a, uint64_t bytes) {
     return aligned && (a.m <= 8 || (a.m <= 16 && a.kt <= 64));
 }
 
+// Shares of the columns over workgroups: where the blocks of outputs (16 rows, up
+// to 64 tokens) leave half of the compute units or more idle and every share
+// keeps 32 tiles; up to four tokens, whose blocks are sooner done, from 128 tiles
+// on.  The sums' second launch takes 2 us.
+uint64_t splits_of(uint64_t m, uint64_t nt, uint64_t kt) {
+    const uint64_t blocks = nt * tiles_of(m, m <= 16 ? 16 : m <= 32 ? 32 : 64);
+    const uint64_t idle = (uint64_t)device_cu_count() / blocks, most = kt / (m <= 4 ? 64 : 32);
+    const uint64_t s = idle < most ? idle : most;
+    return s < 2 ? 1 : s < 8 ? s : 8;
+}
+uint64_t parts_bytes(uint64_t m, uint64_t nt, uint64_t kt) {
+    const uint64_t s = splits_of(m, nt, kt);
+    return s > 1 ? s * m * nt * 64 : 0;
+}
+
 // Whether the form for many tokens takes it.  A round of its workgroups (64 x 256
 // outputs a compute unit) takes about 8/3 as long as one here (64 x 32):
 // 8192 x 8192 bf16, 65 to 128 tokens, 40 us here and 57 there; 300 tokens, 98 and
@@ -424,16 +461,24 @@ bool many(const MatvecArgs& a) {
 
 }  // namespace
 
-uint64_t matvec_w4_workspace(uint64_t m, uint64_t, uint64_t k) {
+namespace {
+uint64_t laying_bytes(uint64_t m, uint64_t kt) {   // what no address needs is not asked for
+    return m <= 4 || (m <= 8 && kt <= 16) ? 0 : laid_bytes(m, kt);
+}
+}  // namespace
+
+uint64_t matvec_w4_workspace(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t kt = tiles_of(k, TILE_COLS);
-    return m <= 4 || (m <= 8 && kt <= 16) ? 0 : laid_bytes(m, kt);   // what no address needs is not asked for
+    return m ? laying_bytes(m, kt) + parts_bytes(m, tiles_of(n, TILE_ROWS), kt) : 0;
 }
 
 int launch_matvec_w4(const MatvecW4& m, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const uint64_t nt = tiles_of(m.n, TILE_ROWS), kt = tiles_of(m.k, TILE_COLS);
     const MatvecArgs a{m.x, m.xscale, reinterpret_cast<const u32x4*>(m.tiles), m.scales, m.y, m.ws, m.x_stride,
-                       m.y_stride, m.n, m.k, m.m, (uint32_t)tiles_of(m.n, TILE_ROWS), (uint32_t)tiles_of(m.k, TILE_COLS),
-                       m.xscale_stride, m.y_type};
+                       m.y_stride, m.n, m.k, m.m, (uint32_t)nt, (uint32_t)kt, m.xscale_stride, m.y_type,
+                       (uint32_t)splits_of(m.m, nt, kt),
+                       reinterpret_cast<float*>(static_cast<char*>(m.ws) + laying_bytes(m.m, kt))};
     const bool rows = in_rows(a, elem_bytes(m.x_type));
     if (!rows) {
         const bool are_many = many(a);

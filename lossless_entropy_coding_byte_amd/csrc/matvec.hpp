@@ -180,6 +180,8 @@ struct MatvecArgs {
     uint64_t x_stride, y_stride, n, k, m;
     uint32_t nt, kt;
     int xscale_stride, y_type;
+    uint32_t splits;   // shares of the columns over workgroups; above 1, sums go to `parts`
+    float* parts;      // [splits][m][16 nt]
 };
 
 // The last step of a sum: the token's factor, one rounding, four outputs.

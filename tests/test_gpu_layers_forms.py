@@ -142,6 +142,23 @@ def test_few_tokens_by_alignment(m, k, dtype):
         assert torch.equal(y, ref), (pad, start)
 
 
+@pytest.mark.parametrize("m", [1, 4, 7, 12, 16, 20, 40, 70])
+@pytest.mark.parametrize("n,k", [(7, 28672), (300, 9000), (40, 20001)])
+@pytest.mark.parametrize("dtype", [I8, BF16], ids=str)
+def test_few_rows_and_many_columns(m, n, k, dtype):
+    """Columns shared out over workgroups, the last share shorter, its last tile partial; strided rows, same bits."""
+    q, s, w4 = weights(n, k, 128, BF16, m + k)
+    x, xs = tokens(m, k, dtype, m * k)
+    xd, xsd = x.to(DEV), None if xs is None else xs.to(DEV)
+    y = lecb.matvec_w4(xd, w4, x_scale=xsd, out_dtype=F32)
+    check_matvec(y, x, xs, q, s, 128)
+    big = torch.zeros(m, k + 3, dtype=dtype, device=DEV)
+    big[:, 1 : k + 1] = xd
+    for _ in range(2):
+        assert torch.equal(y, lecb.matvec_w4(big[:, 1 : k + 1], w4, x_scale=xsd, out_dtype=F32))
+    assert torch.equal(y.to(BF16), lecb.matvec_w4(xd, w4, x_scale=xsd, out_dtype=BF16))
+
+
 def test_workspace_of_the_caller():
     """A workspace kept by the caller, its contents of no matter; calls with less are refused."""
     q, s, w4 = weights(80, 512, 64, BF16, 11)
