@@ -114,8 +114,8 @@ __device__ inline float of_quad(float v) {   // lane I's of each four
 // into the tile's order, so that it leaves in one store.
 //
 // Bound by HBM, with the vector instructions (about 9 a weight) close behind:
-// 8192 x 8192 bf16, groups of 128, 38 us, 4.4 TB/s; fp32, groups of 64, 60 us,
-// 5.0 TB/s (as a large copy).  By 64-byte pieces of 16 rows, as the tile lies,
+// 8192 x 8192 bf16, groups of 128, 37 us, 4.6 TB/s; fp32, groups of 64, 59 us,
+// 5.2 TB/s (a large copy: 5.0).  By 64-byte pieces of 16 rows, as the tile lies,
 // the loads and fourteen instructions a weight took 46 and 72 us.
 template <typename T, int GROUP>
 __global__ __launch_bounds__(256) void quantize_w4_kernel(const T* __restrict__ w, uint64_t stride, uint64_t n,
@@ -175,7 +175,7 @@ __device__ inline float code_value(uint32_t word, int i) { return (float)((int)(
 
 // A wave a tile; its words go through LDS to lanes that write four whole rows'
 // columns at a time, as in quantize_w4_kernel.  Bound by the writes: 8192 x 8192 to
-// bf16 in 28 us, 6 TB/s with the codes (30 by 64-byte pieces of 16 rows).
+// bf16 in 27 us, 6.2 TB/s with the codes (30 by 64-byte pieces of 16 rows).
 template <typename T, int GROUP>
 __global__ __launch_bounds__(256) void dequantize_w4_kernel(const u32x4* __restrict__ in,
                                                             const void* __restrict__ scales, int bf16, uint64_t n,
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(256) void untile_w4_kernel(const u32x4* __restrict_
 // cancels, so the sum of squares and the maximum come out of one pass and one
 // reduction.  The order of the sums depends on the number of columns alone.
 //
-// Bound by HBM: 16384 x 2048 bf16 with the residual 41 us, 5.7 TB/s of what it
+// Bound by HBM: 16384 x 2048 bf16 with the residual 40 us, 5.8 TB/s of what it
 // reads and writes; 4096 x 8192 fp32 86 us, 5.0 TB/s; one row of 4096 takes
 // 3.4 us, two memory latencies and the reduction.
 template <int THREADS>
