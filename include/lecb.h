@@ -612,7 +612,8 @@ int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const fl
  * or d_xscale[0] (stride 0); rounded once to y_type (F32, BF16, F16).
  *   x: x_type I8, BF16 or F16, row stride x_stride; d_xscale: only for I8,
  *   NULL = 1.
- * 16-bit x: scales of 2^116 and more are infinite.
+ * 16-bit x: scales of 2^116 and more are infinite, and a token with an infinity
+ * or NaN gives NaN (its offset's sum is one too; see Operand in matvec.hpp).
  * The result does not depend on what else runs, and a token's row not on the
  * other rows' values.
  * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken); its
