@@ -612,8 +612,11 @@ int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const fl
  * or d_xscale[0] (stride 0); rounded once to y_type (F32, BF16, F16).
  *   x: x_type I8, BF16 or F16, row stride x_stride; d_xscale: only for I8,
  *   NULL = 1.
- * 16-bit x: scales of 2^116 and more are infinite, and a token with an infinity
- * or NaN gives NaN (its offset's sum is one too; see Operand in matvec.hpp).
+ * 16-bit x: every product is exact, so the error of a sum is at most
+ * (2 group + groups + 24) 2^-24 of the sum of |x q s| before the last rounding;
+ * a column whose code is 0 adds nothing to it, however large x is there.
+ * Infinities and NaN in x do what the formula says (an infinity times 0 is NaN).
+ * BF16 x: scales of 2^118 and more are infinite.
  * The result does not depend on what else runs, and a token's row not on the
  * other rows' values.
  * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken); its

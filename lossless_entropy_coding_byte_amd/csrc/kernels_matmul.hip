@@ -9,11 +9,6 @@ namespace {
 
 // ---------------------------------------------------------------- tokens laid out
 
-template <int CTRL>
-__device__ inline float add_lanes(float v) {   // v + the v of the lane that CTRL names
-    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-
 // A workgroup takes 16 tokens and the columns of 256 units: one tile of 16-bit
 // tokens, two of bytes.  Lanes read along the tokens' rows and write along the
 // pieces, through LDS (the XOR spreads both over the banks).
@@ -24,7 +19,7 @@ __device__ inline float add_lanes(float v) {   // v + the v of the lane that CTR
 // order and sums of the tokens made once instead of by every workgroup.  Bound by
 // latency: 512 x 8192 bf16 6 us, 32 x 8192 int8 2.6 us.
 template <typename X, bool MANY>
-__global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t group, uint32_t across) {
+__global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t across) {
     typedef Operand<X> O;
     typedef Tokens<X> T;
     constexpr int TILES = 16 / T::UNITS;
@@ -37,19 +32,6 @@ __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t 
     if (t < a.m && tk < a.kt) {
         const X* p = reinterpret_cast<const X*>(a.x) + t * a.x_stride + col;
         v = O::order(col + TILE_COLS <= a.k ? T::load(p, unit) : T::load(p, unit, (uint32_t)(a.k - col)));
-    }
-    if constexpr (O::OFFSET && MANY) {
-        // 16 neighbouring lanes hold a token's tile, group / 8 of them a group
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = O::dot(v[i], O::EXCESS, s);
-        s = add_lanes<0xB1>(s);                     // the next lane's
-        s = add_lanes<0x4E>(s);                     // the next two's
-        if (group >= 64) s = add_lanes<0x141>(s);   // mirrored within eight
-        if (group >= 128) s = add_lanes<0x140>(s);  // mirrored within sixteen
-        const uint32_t per = group / 8, groups = 16 / per;
-        if (tk < a.kt && unit % per == 0)
-            laid_sums<X>(a)[(((uint64_t)(mt / 4) * a.kt + tk) * groups + unit / per) * 64 + mt % 4 * 16 + token] = s;
     }
     sh[(sub * T::UNITS + unit) * 16 + (token ^ unit)] = v;
     __syncthreads();
@@ -76,7 +58,6 @@ struct MmTile {
     static constexpr int SCALES = GROUPS * 4 * 16, LOADS = SCALES * sizeof(S) < 256 ? 1 : SCALES * sizeof(S) / 256;
     u32x4 x[2 * PIECES][64];
     S scales[WN][LOADS * 256 / sizeof(S)];                // [4][groups][16 rows]
-    float excess[Operand<X>::OFFSET ? GROUPS : 1][64];    // of each token
 };
 
 // Sends for a tile while another is computed.  The compiler keeps the reads
@@ -96,9 +77,11 @@ __device__ __forceinline__ void mm_step(const Tile* __restrict__ now, Tile* __re
 // number is what counts, and these take half as many as 16 x 16 ones.
 //
 // Bound by that issue: of 16-bit tokens, a tile of 128 columns costs a wave 32
-// matrix instructions (1024 cycles), about 200 vector ones (128 for its words,
-// 64 a group for the scales) and 40 others.  512 x 8192 x 8192 bf16: groups of
-// 128 69 us, 1000 TFLOP/s, of 64 74, of 32 91; int8, groups of 128, 46 us (the
+// matrix instructions (1024 cycles), about 280 vector ones (208 for its words,
+// 64 a group for the scales) and 90 others.  512 x 8192 x 8192 with the layout of
+// the tokens, bf16: groups of 128 80 us, of 64 81, of 32 94; operands with an
+// offset (Operand), which eight instructions a word make instead of 13 but whose
+// sums are read from LDS for every group: 77, 88 and 99.  int8, groups of 128, 51 us (the
 // library's product of two bf16 matrices of 8192 x 8192: 1250 TFLOP/s).  Tried
 // and slower: one matrix instruction, then a share of the vector ones, in turn
 // (+ 15 %, as then neither wave of a SIMD runs ahead); all words' numbers before
@@ -144,7 +127,6 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
         scale_offset[q] = (uint32_t)(tile_row(b / ROW) - tile_row(0)) * a.kt * ROW + b % ROW;
     }
     const u32x4* from_x = laid_tokens(a) + (uint64_t)mb * a.kt * (2 * PIECES * 64);
-    const float* from_excess = laid_sums<X>(a) + (uint64_t)mb * a.kt * (GROUPS * 64);
 
     auto fetch_words = [&](Words& w, uint32_t tk) __attribute__((always_inline)) {
 #pragma unroll
@@ -153,19 +135,17 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
             for (int s = 0; s < 2; ++s) w.v[j][s] = from_words[j][(uint64_t)tk * 64 + s * 16];
         asm volatile("" ::: "memory");   // here, not where they are needed
     };
-    constexpr int SENDS = 2 * PIECES / WN + Tile::LOADS + (O::OFFSET ? 1 : 0);
+    constexpr int SENDS = 2 * PIECES / WN + Tile::LOADS;
     auto send = [&](uint32_t tk, Tile* tile, int i) __attribute__((always_inline)) {
-        constexpr int A = 2 * PIECES / WN, B = A + Tile::LOADS;
+        constexpr int A = 2 * PIECES / WN;
         if (i < A) {
             // piece p of the two blocks of 32 tokens, which lie a.kt tiles apart
             const uint32_t p = i * WN + wn;
             load_to_lds<16>(from_x + ((uint64_t)(p / PIECES) * a.kt + tk) * (PIECES * 64) + p % PIECES * 64, 16 * lane,
                             tile->x[p]);
-        } else if (i < B) {
+        } else {
             load_to_lds<4>(from_scales + (uint64_t)tk * ROW, scale_offset[i - A],
                            &tile->scales[wn][(i - A) * (256 / sizeof(S))]);
-        } else {   // by several waves alike
-            load_to_lds<4>(from_excess + ((uint64_t)tk * GROUPS + wn % GROUPS) * 64, 4 * lane, tile->excess[wn % GROUPS]);
         }
     };
 
@@ -200,19 +180,9 @@ __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, 
                     if (q * UNITS / SENDS == g * 2 + j) send(ahead, next, q);
                 Acc acc[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (O::OFFSET) {   // token 32 i + 8 q + 4 h + e
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const f32x4 v = *reinterpret_cast<const f32x4*>(&now->excess[g][32 * i + 8 * q + 4 * h]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][4 * q + e] = v[e];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[i][e] = 0;
-                    }
-                }
+                    for (int e = 0; e < 16; ++e) acc[i][e] = 0;
                 if constexpr (sizeof(X) == 2) {
 #pragma unroll
                     for (int p = 0; p < N; ++p) {
@@ -329,14 +299,14 @@ int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s
 }
 
 template <typename X>
-int lay_as(const MatvecArgs& a, uint32_t group, bool many, hipStream_t s) {
+int lay_as(const MatvecArgs& a, bool many, hipStream_t s) {
     const uint64_t across = tiles_of(a.kt, 16 / Tokens<X>::UNITS);
     const uint64_t blocks = across * (many ? tiles_of(a.m, LAID_TOKENS) * (LAID_TOKENS / 16) : tiles_of(a.m, 16));
     if (blocks >= 1u << 31) return LECB_ERR_TOO_LARGE;
     if (many)
-        lay_tokens_kernel<X, true><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, group, (uint32_t)across);
+        lay_tokens_kernel<X, true><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, (uint32_t)across);
     else
-        lay_tokens_kernel<X, false><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, group, (uint32_t)across);
+        lay_tokens_kernel<X, false><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, (uint32_t)across);
     return launched();
 }
 
@@ -347,11 +317,11 @@ uint64_t matmul_w4_turns(const MatvecArgs& a) {
     return a8 < a4 ? a8 : a4;
 }
 
-int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s) {
+int launch_lay_tokens(const MatvecArgs& a, int x_type, bool many, hipStream_t s) {
     switch (x_type) {
-        case LECB_I8: return lay_as<int8_t>(a, group, many, s);
-        case LECB_BF16: return lay_as<__bf16>(a, group, many, s);
-        default: return lay_as<_Float16>(a, group, many, s);
+        case LECB_I8: return lay_as<int8_t>(a, many, s);
+        case LECB_BF16: return lay_as<__bf16>(a, many, s);
+        default: return lay_as<_Float16>(a, many, s);
     }
 }
 

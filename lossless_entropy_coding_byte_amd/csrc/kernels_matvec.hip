@@ -103,15 +103,7 @@ struct Sums {
         } else {
             constexpr int N = WORDS == 1 ? 1 : 2;   // words of a group in this half
 #pragma unroll
-            for (int g = 0; g < 2 / N; ++g) {
-                const u32x4 over = {O::EXCESS, O::EXCESS, O::EXCESS, O::EXCESS};
-                Acc none[MT];
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    none[i] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int d = 0; d < N; ++d) none[i] = O::mul(h.x[i][g * N + d], over, none[i]);
-                }
+            for (int g = 0; g < 2 / N; ++g)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     u32x4 q[N];
@@ -120,17 +112,15 @@ struct Sums {
                     const float s = w.scale[j * GROUPS + (WORDS == 4 ? 0 : H * GROUPS / 2 + g)];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        Acc v = WORDS == 4 && H == 1 ? acc[i][j] : none[i];
+                        Acc v = WORDS == 4 && H == 1 ? acc[i][j] : Acc{0, 0, 0, 0};
 #pragma unroll
                         for (int d = 0; d < N; ++d) v = O::mul(h.x[i][g * N + d], q[d], v);
-                        if (WORDS == 4 && H == 1) v += none[i];
                         if (WORDS == 4 && H == 0)
                             acc[i][j] = v;
                         else
                             finish(i, j, v, s);
                     }
                 }
-            }
         }
     }
 };
@@ -482,7 +472,7 @@ int launch_matvec_w4(const MatvecW4& m, void* stream) {
     const bool rows = in_rows(a, elem_bytes(m.x_type));
     if (!rows) {
         const bool are_many = many(a);
-        const int rc = launch_lay_tokens(a, m.x_type, m.group, are_many, s);
+        const int rc = launch_lay_tokens(a, m.x_type, are_many, s);
         if (rc) return rc;
         if (are_many) return launch_matmul_w4(a, m.x_type, m.scale_type, m.group, s);
     }

@@ -23,35 +23,50 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // any order that both sides share.
 //
 // bytes: a code's four bits as the upper half of a byte, 16 q, the even
-// columns and the odd ones in a register each.
+// columns and the odd ones in a register each.  FACTOR, of the result, undoes 16.
 //
-// 16 bits: a code's four bits, the sign's turned over, as the upper bits of the
-// mantissa of 2^-8: 2^-8 (1 + (q + 8) / 16), exactly, for one logic operation a
-// pair of codes (columns p and p + 4) after one shift; a conversion to float
-// and a packing take four times as long.  What is too much, 1.5 2^-8 times the
-// group's sum of x, is put into the sum beforehand: by an instruction whose
-// second operand is EXCESS, or from sums made before (Tokens).  2^-8 keeps the
-// sum over a group within the range of x, exact for its smallest numbers too.
-// SCALE, of a group's scale, undoes 16 and 2^-8; FACTOR, of the result, 16.
+// 16 bits: every code as the number it is, for errors that follow the sum of
+// |x q|: a column whose code is 0 adds nothing, however large x is there.  A
+// code's magnitude (0..8) and sign in a byte are the e4m3 number q 2^-9, as
+// that type's numbers are evenly spaced up to 2^-5: nine logic operations and
+// additions make the bytes of eight codes, four conversions (scaled, exact) their
+// pairs.  (An offset that turns a code's bits into a number's by one operation a
+// pair takes eight in all, but has to cancel out of the sums: 24 times the
+// tokens', whose rounding is left.)
+//
+// bf16: q 2^-10 keeps a group's sum (128 x 8) within the range of x; its
+// smallest numbers' products, multiples of 2^-143, are still exact.  SCALE, of a
+// group's scale, undoes it.  fp16: q, as no sum of it leaves the range.
 template <typename X>
 struct Operand;
 
-// Pairs of halves (p, p + 4), p = 0..3, out of eight halves in order.
+// The bytes described above: of the even columns and of the odd ones.  Three-input
+// logic operations take half as long as the and-ors that the compiler makes of this.
+__device__ inline u32x2 code_bytes(uint32_t w) {
+    constexpr uint32_t PICK = 0xE4, TURN = 0x6C;   // c ? a : b and (a & c) ^ b, bit by bit
+    const uint32_t sign = w & 0x88888888u, one = sign >> 3;
+    const uint32_t size = __builtin_amdgcn_bitop3_b32(w, sign - one, 0x77777777u, TURN) + one;
+    return {(uint32_t)__builtin_amdgcn_bitop3_b32(size, sign << 4, 0x0F0F0F0Fu, PICK),
+            (uint32_t)__builtin_amdgcn_bitop3_b32(size >> 4, sign, 0x0F0F0F0Fu, PICK)};
+}
+// Eight halves in the order of those bytes' pairs: 0 2, 4 6, 1 3, 5 7.
 __device__ inline u32x4 pairs_of_halves(u32x4 x) {
-    return {__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
-            __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
+    return {__builtin_amdgcn_perm(x.y, x.x, 0x05040100u), __builtin_amdgcn_perm(x.w, x.z, 0x05040100u),
+            __builtin_amdgcn_perm(x.y, x.x, 0x07060302u), __builtin_amdgcn_perm(x.w, x.z, 0x07060302u)};
 }
 
 template <>
 struct Operand<__bf16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float SCALE = 4096.0f, FACTOR = 1.0f;
-    static constexpr bool OFFSET = true;
-    static constexpr uint32_t EXCESS = 0xBBC0BBC0u;   // -1.5 2^-8, twice
+    static constexpr float SCALE = 1024.0f, FACTOR = 1.0f;
     static __device__ A weights(uint32_t w) {
-        return {((w << 3) & 0x00780078u) ^ 0x3BC03BC0u, ((w >> 1) & 0x00780078u) ^ 0x3BC03BC0u,
-                ((w >> 5) & 0x00780078u) ^ 0x3BC03BC0u, ((w >> 9) & 0x00780078u) ^ 0x3BC03BC0u};
+        const u32x2 b = code_bytes(w);
+        auto pair = [](bf16x2 v) { return __builtin_bit_cast(uint32_t, v); };
+        return {pair(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b.x, 0.5f, false)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b.x, 0.5f, true)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b.y, 0.5f, false)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b.y, 0.5f, true))};
     }
     static __device__ u32x4 order(u32x4 x) { return pairs_of_halves(x); }
     static __device__ Acc mul(A a, A b, Acc c) {
@@ -62,20 +77,19 @@ struct Operand<__bf16> {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
     }
-    static __device__ float dot(uint32_t a, uint32_t b, float c) {
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
-    }
 };
 template <>
 struct Operand<_Float16> {
     typedef u32x4 A;
     typedef f32x4 Acc;
-    static constexpr float SCALE = 4096.0f, FACTOR = 1.0f;
-    static constexpr bool OFFSET = true;
-    static constexpr uint32_t EXCESS = 0x9E009E00u;
+    static constexpr float SCALE = 1.0f, FACTOR = 1.0f;
     static __device__ A weights(uint32_t w) {
-        return {((w << 6) & 0x03C003C0u) ^ 0x1E001E00u, ((w << 2) & 0x03C003C0u) ^ 0x1E001E00u,
-                ((w >> 2) & 0x03C003C0u) ^ 0x1E001E00u, ((w >> 6) & 0x03C003C0u) ^ 0x1E001E00u};
+        const u32x2 b = code_bytes(w);
+        auto pair = [](f16x2 v) { return __builtin_bit_cast(uint32_t, v); };
+        return {pair(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b.x, 512.0f, false)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b.x, 512.0f, true)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b.y, 512.0f, false)),
+                pair(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b.y, 512.0f, true))};
     }
     static __device__ u32x4 order(u32x4 x) { return pairs_of_halves(x); }
     static __device__ Acc mul(A a, A b, Acc c) {
@@ -86,16 +100,12 @@ struct Operand<_Float16> {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
     }
-    static __device__ float dot(uint32_t a, uint32_t b, float c) {
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
-    }
 };
 template <>
 struct Operand<int8_t> {
     typedef u32x2 A;
     typedef i32x4 Acc;
     static constexpr float SCALE = 1.0f, FACTOR = 0.0625f;
-    static constexpr bool OFFSET = false;
     static __device__ A weights(uint32_t w) { return {(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u}; }
     static __device__ u32x2 order(u32x2 x) {
         return {__builtin_amdgcn_perm(x.y, x.x, 0x06040200u), __builtin_amdgcn_perm(x.y, x.x, 0x07050301u)};
@@ -243,22 +253,15 @@ __device__ inline void loads_done() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N
 //                         takes unit 4 p + c of token r;
 //   many, 32 x 32:        [32 tokens][kt][2 PIECES: 2 p + s][64 lanes]: lane
 //                         32 h + r takes unit 4 p + 2 h + s of token r.
-// For 16 bits also -1.5 2^-8 times each group's sum of each token, [64 tokens]
-// [kt][groups][64].  Tokens past m and columns past k are zeros.
+// Tokens past m and columns past k are zeros.
 constexpr int LAID_TOKENS = 64;   // the workspace holds a multiple of these
 __host__ __device__ inline uint64_t laid_units(uint64_t m, uint64_t kt, uint64_t bytes) {
     return (m + LAID_TOKENS - 1) / LAID_TOKENS * LAID_TOKENS * kt * (8 * bytes);
 }
-inline uint64_t laid_bytes(uint64_t m, uint64_t kt) {   // of the widest type, with sums of the smallest groups
-    return laid_units(m, kt, 2) * 16 + (m + LAID_TOKENS - 1) / LAID_TOKENS * LAID_TOKENS * kt * (4 * 4);
-}
+inline uint64_t laid_bytes(uint64_t m, uint64_t kt) { return laid_units(m, kt, 2) * 16; }   // of the widest type
 inline __device__ const u32x4* laid_tokens(const MatvecArgs& a) { return reinterpret_cast<const u32x4*>(a.ws); }
-template <typename X>
-__device__ inline float* laid_sums(const MatvecArgs& a) {
-    return reinterpret_cast<float*>(reinterpret_cast<u32x4*>(a.ws) + laid_units(a.m, a.kt, sizeof(X)));
-}
 
-int launch_lay_tokens(const MatvecArgs& a, int x_type, uint32_t group, bool many, hipStream_t s);
+int launch_lay_tokens(const MatvecArgs& a, int x_type, bool many, hipStream_t s);
 constexpr uint32_t MM_TILES = 1u << 22;   // more tiles of columns than this: in the form for few tokens
 uint64_t matmul_w4_turns(const MatvecArgs& a);   // its time, in 64 x 64 outputs of a wave
 int launch_matmul_w4(const MatvecArgs& a, int x_type, int scale_type, uint32_t group, hipStream_t s);

@@ -166,8 +166,8 @@ def dequantize_q8(q, scale, dtype=torch.bfloat16):
 def matvec_w4(x, w4: W4Weights, x_scale=None, out_dtype=None, ws=None):
     """y = x W^T for tokens x [..., k] of int8 (x_scale: float32, one per row or one), bfloat16 or float16.
 
-    Returns y [..., n] of out_dtype (x's type; bfloat16 for int8 x).  A token of
-    16 bits with an infinity or NaN gives NaN, and no other token does.  ws: a
-    uint8 workspace of lecb_matvec_w4_workspace_bytes that the caller keeps;
-    calls that overlap in time must not share one."""
+    Returns y [..., n] of out_dtype (x's type; bfloat16 for int8 x).  An infinity
+    or NaN in a token changes that token's results alone.  ws: a uint8 workspace
+    of lecb_matvec_w4_workspace_bytes that the caller keeps; calls that overlap in
+    time must not share one."""
     return _tensors.matvec_w4(x, w4.tiles, w4.scales, w4.n, w4.k, w4.group, x_scale, out_dtype, ws)
