@@ -261,6 +261,8 @@ PyObject* matvec_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         const at::ScalarType yt =
             args[7] != Py_None ? dtype(args[7], "matvec_w4: out_dtype") : xt == at::kChar ? at::kBFloat16 : xt;
         check(is_float(yt), yt, "matvec_w4: out_dtype");
+        if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))
+            refuse("matvec_w4: ws is contiguous uint8");
         const Here here(x, tiles, scales, xscale, ws);
         at::DimVector size(x.sizes());
         size.back() = n;

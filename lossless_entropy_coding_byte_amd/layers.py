@@ -80,6 +80,8 @@ def lecb_dequantize_q8(q, rows, cols, scale, scale_stride, out, stream=None) -> 
 
 def lecb_matvec_w4(x, x_stride, x_scale, x_scale_stride, m, tiles, scales, group, n, k, y, y_stride, ws=None,
                    stream=None) -> None:
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("lecb_matvec_w4: ws is contiguous")
     _check(load().lecb_matvec_w4(_ptr(x), _TYPES[x.dtype], x_stride, _ptr(x_scale), x_scale_stride, m, _ptr(tiles),
                                  _ptr(scales), _TYPES[scales.dtype], group, n, k, _ptr(y), _TYPES[y.dtype], y_stride,
                                  _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
