@@ -118,6 +118,18 @@ void done(int status, const char* where) {
 }
 int64_t up(int64_t n, int64_t step) { return n / step + (n % step != 0); }
 
+// Weights as the kernels take them on trust: their fields may have been set since
+// W4Weights checked them.
+void check_weights(const at::Tensor& tiles, const at::Tensor& scales, int64_t n, int64_t k, int64_t group) {
+    constexpr int64_t END = int64_t(1) << 31;
+    if (n < 1 || k < 1 || n >= END || k >= END || (group != 32 && group != 64 && group != 128))
+        refuse("weights: n and k are at least 1, group is 32, 64 or 128");
+    const int64_t cells = up(n, 16) * up(k, 128);
+    if (tiles.scalar_type() != at::kByte || tiles.numel() != cells * 1024 || !tiles.is_contiguous() ||
+        !is_scale(scales.scalar_type()) || scales.numel() != cells * (2048 / group) || !scales.is_contiguous())
+        refuse("weights: tiles and scales are not those of n, k and group");
+}
+
 // Runs the body of an entry: C++ exceptions become Python's.
 template <typename F>
 PyObject* entry(Py_ssize_t have, Py_ssize_t want, F body) {
@@ -248,6 +260,7 @@ PyObject* matvec_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         const at::Tensor& tiles = tensor(args[1], name);
         const at::Tensor& scales = tensor(args[2], name);
         const int64_t n = integer(args[3]), k = integer(args[4]), group = integer(args[5]);
+        check_weights(tiles, scales, n, k, group);
         const at::Tensor xscale = optional(args[6], "matvec_w4: x_scale");
         at::Tensor ws = optional(args[8], "matvec_w4: ws");
         const Rows xr(x, name);
@@ -319,6 +332,7 @@ PyObject* dequantize_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         const at::Tensor& tiles = tensor(args[0], name);
         const at::Tensor& scales = tensor(args[1], name);
         const int64_t group = integer(args[2]), n = integer(args[3]), k = integer(args[4]);
+        check_weights(tiles, scales, n, k, group);
         const at::ScalarType t = dtype(args[5], name);
         check(is_float(t), t, name);
         const Here here(tiles, scales);
