@@ -108,6 +108,35 @@ struct Rows {
     }
 };
 
+// Memory that rows take up.
+struct Area {
+    uint64_t begin, rows, bytes, stride;   // of a row, from one to the next
+    Area(const at::Tensor& t, uint64_t rows, uint64_t cols, uint64_t row_stride)
+        : begin(reinterpret_cast<uintptr_t>(t.data_ptr())), rows(rows), bytes(cols * t.element_size()),
+          stride(row_stride * t.element_size()) {}
+    bool operator==(const Area& o) const { return begin == o.begin && stride == o.stride && bytes == o.bytes; }
+    uint64_t end() const { return begin + (rows - 1) * stride + bytes; }
+    // The first of the rows that ends past `at`.
+    uint64_t first_past(uint64_t at) const {
+        return begin + bytes > at ? 0 : (at - begin - bytes) / stride + 1;
+    }
+    // Whether any row meets one of o's.  Rows of two areas may lie in turn, as the
+    // columns of one buffer do.  With one stride, what holds for a row of o holds for
+    // those after it, so the first that ends past this area's begin, and the one after
+    // it, which begins there, tell; otherwise one row after another is looked at.
+    bool meets(const Area& o) const {
+        if (!rows || !o.rows || end() <= o.begin || o.end() <= begin) return false;
+        if (rows == 1 && o.rows > 1) return o.meets(*this);
+        const uint64_t from = o.first_past(begin);
+        for (uint64_t j = from; j < o.rows && o.begin + j * o.stride < end(); ++j) {
+            if (o.stride == stride && j > from + 1) break;
+            const uint64_t at = o.begin + j * o.stride, i = first_past(at);
+            if (i < rows && begin + i * stride < at + o.bytes) return true;
+        }
+        return false;
+    }
+};
+
 at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) {
     // what at::empty comes to on a GPU, without its dispatch
     return at::Tensor(at::detail::empty_cuda(size, t, like.device(), std::nullopt));
@@ -198,17 +227,24 @@ PyObject* rmsnorm_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
         if (fixed && (scale.scalar_type() != at::kFloat || scale.numel() != 1))
             refuse("rmsnorm_q8: a fixed scale is one float32 number");
         if (given && !residual.defined()) refuse("rmsnorm_q8: without a residual h is x");
-        const Here here(x, weight, residual, scale, h);
-        int64_t rs = 0, hs = 0;
+        int64_t rs = 0, hs = xr.cols;
         if (residual.defined()) {
             if (residual.sizes() != x.sizes() || residual.scalar_type() != x.scalar_type())
                 refuse("rmsnorm_q8: residual has x's shape and type");
             rs = Rows(residual, "rmsnorm_q8: residual").stride;
-            if (!given) h = make(x.sizes(), x.scalar_type(), x);
+        }
+        if (given) {
             if (h.sizes() != x.sizes() || h.scalar_type() != x.scalar_type())
                 refuse("rmsnorm_q8: out_h has x's shape and type");
             hs = Rows(h, "rmsnorm_q8: out_h").stride;
+            const uint64_t rows = xr.rows, cols = xr.cols;
+            const Area area(h, rows, cols, hs), ax(x, rows, cols, xr.stride), ar(residual, rows, cols, rs);
+            if ((!(area == ax) && area.meets(ax)) || (!(area == ar) && area.meets(ar)) ||
+                area.meets(Area(weight, 1, cols, cols)) || (fixed && area.meets(Area(scale, 1, 1, 1))))
+                refuse("rmsnorm_q8: out_h overlaps what is read, other than as x or residual in place");
         }
+        const Here here(x, weight, residual, scale, h);
+        if (residual.defined() && !given) h = make(x.sizes(), x.scalar_type(), x);
         if (!fixed) scale = make(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
         const at::Tensor q = make(x.sizes(), at::kChar, x);
         void* stream = here.stream();

@@ -42,3 +42,56 @@ def test_weights_changed_after_they_were_made(field, value):
     x = torch.zeros(1, bad.k if 0 < bad.k else 1, dtype=BF16)
     with pytest.raises(ValueError, match="weights"):
         lecb.matvec_w4(x, bad)
+
+
+def _windows():
+    """(x, residual, out_h) in buffers of their own or in one."""
+    buf, other = torch.zeros(4096, dtype=BF16), torch.zeros(4096, dtype=BF16)
+
+    def at(b, start, stride, rows=8, cols=32):
+        return b.as_strided((rows, cols), (stride, 1), start)
+
+    for start, stride in ((32, 32), (1, 32), (0, 64), (7 * 32, 32), (31, 64), (32, 64), (33, 64), (7 * 64 + 31, 64), (64, 40)):
+        yield at(buf, 0, 32 if stride == 32 else 64), at(other, 0, 32), at(buf, start, stride)
+    x = at(buf, 1024, 64)
+    for start, stride in ((1024, 64), (1024 + 32, 64), (1024 - 32, 64), (1024 + 96, 64), (1024 + 65, 64), (1024 - 33, 64),
+                          (1024 - 7 * 64 - 31, 64), (1024 - 7 * 64 - 32, 64), (1024 - 8 * 64, 64), (1024 + 8 * 64, 64),
+                          (0, 128), (1024 + 32, 128), (1024 - 32, 128), (1024 + 33, 128), (1024 + 7 * 64 + 32, 32),
+                          (1024 + 7 * 64 + 31, 32), (800, 96), (832, 96)):
+        yield x, at(other, 0, 32), at(buf, start, stride)
+        yield at(other, 0, 32), x, at(buf, start, stride)
+
+
+@pytest.mark.parametrize("x,residual,out", list(_windows()), ids=lambda t: f"{t.storage_offset()}/{t.stride(0)}")
+def test_result_over_other_rows(x, residual, out):
+    """h may stand where x or the residual stand, row for row; over other rows of theirs it would
+    be written while they are read.  Rows beside them in one buffer are not over them."""
+
+    def places(t):
+        return {t.untyped_storage().data_ptr() + 2 * (t.storage_offset() + r * t.stride(0) + c)
+                for r in range(8) for c in range(32)}
+
+    def same(t):
+        return t.data_ptr() == out.data_ptr() and t.stride() == out.stride()
+
+    meets = any(not same(t) and bool(places(t) & places(out)) for t in (x, residual))
+    with pytest.raises(ValueError, match="out_h overlaps" if meets else "current GPU"):
+        lecb.rmsnorm_q8(x, torch.ones(32, dtype=BF16), residual=residual, out_h=out)
+
+
+def test_result_over_the_weight_or_the_scale():
+    buf = torch.zeros(1024, dtype=BF16)
+    x, r, out = torch.zeros(8, 32, dtype=BF16), torch.zeros(8, 32, dtype=BF16), buf[64:320].view(8, 32)
+    for start in (33, 64, 200, 319):
+        with pytest.raises(ValueError, match="out_h overlaps"):
+            lecb.rmsnorm_q8(x, buf[start : start + 32], residual=r, out_h=out)
+    for start in (32, 320):
+        with pytest.raises(ValueError, match="current GPU"):
+            lecb.rmsnorm_q8(x, buf[start : start + 32], residual=r, out_h=out)
+    with pytest.raises(ValueError, match="out_h overlaps"):
+        lecb.rmsnorm_q8(x, torch.ones(32), residual=r, out_h=out, scale=buf[100:102].view(torch.float32))
+    wide = buf[:512].view(8, 64)[:, :32]     # rows 64 apart, the weight between two of them
+    with pytest.raises(ValueError, match="current GPU"):
+        lecb.rmsnorm_q8(x, buf[96:128], residual=r, out_h=wide)
+    with pytest.raises(ValueError, match="out_h overlaps"):
+        lecb.rmsnorm_q8(x, buf[95:127], residual=r, out_h=wide)
