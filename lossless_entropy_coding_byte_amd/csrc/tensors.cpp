@@ -10,8 +10,12 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+#include <memory>
 #include <string>
 
 #include "lecb.h"
@@ -137,6 +141,24 @@ struct Area {
     }
 };
 
+// Whether gradients are being recorded for any of an entry's inputs.  No entry has
+// a derivative; a tangent would be lost without a word, so it is refused.
+template <typename... Ts>
+bool recorded(const char* name, const Ts&... inputs) {
+    if (((inputs.defined() && inputs._fw_grad(0).defined()) || ...))
+        refuse(std::string(name) + ": forward-mode derivatives are not there");
+    return at::GradMode::is_enabled() && ((inputs.defined() && inputs.requires_grad()) || ...);
+}
+
+// Lets a backward pass that reaches `results` end in an error that names the entry.
+template <typename... Ts>
+void no_backward(const char* name, std::initializer_list<at::Tensor> results, const Ts&... inputs) {
+    const std::shared_ptr<torch::autograd::Node> node(new torch::autograd::NotImplemented(name), torch::autograd::deleteNode);
+    node->set_next_edges(torch::autograd::collect_next_edges(inputs...));
+    for (const at::Tensor& r : results)
+        if (r.defined()) torch::autograd::set_history(r, node);
+}
+
 at::Tensor make(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) {
     // what at::empty comes to on a GPU, without its dispatch
     return at::Tensor(at::detail::empty_cuda(size, t, like.device(), std::nullopt));
@@ -227,6 +249,8 @@ PyObject* rmsnorm_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
         if (fixed && (scale.scalar_type() != at::kFloat || scale.numel() != 1))
             refuse("rmsnorm_q8: a fixed scale is one float32 number");
         if (given && !residual.defined()) refuse("rmsnorm_q8: without a residual h is x");
+        const bool grads = recorded(name, x, weight, residual, scale, h);
+        if (grads && given) refuse("rmsnorm_q8: out_h goes with inputs that gradients are not recorded for");
         int64_t rs = 0, hs = xr.cols;
         if (residual.defined()) {
             if (residual.sizes() != x.sizes() || residual.scalar_type() != x.scalar_type())
@@ -256,6 +280,7 @@ PyObject* rmsnorm_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                  static_cast<int8_t*>(ptr(q)), static_cast<float*>(ptr(scale)), fixed, stream);
         }
         done(rc, "lecb_rmsnorm_q8");
+        if (grads) no_backward(name, {fixed ? at::Tensor() : scale, h}, x, weight, residual, scale);
         return tuple(THPVariable_Wrap(q), fixed ? share(args[4]) : THPVariable_Wrap(scale),
                      !residual.defined() ? share(args[0]) : given ? share(args[5]) : THPVariable_Wrap(h));
     });
@@ -274,6 +299,7 @@ PyObject* dequantize_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
         const int64_t cols = q.sizes().back(), rows = cols ? q.numel() / cols : 0;
         if (scale.scalar_type() != at::kFloat || !scale.is_contiguous() || (scale.numel() != 1 && scale.numel() != rows))
             refuse("dequantize_q8: one float32 scale per row, or one");
+        const bool grads = recorded(name, scale);
         const Here here(q, scale);
         const at::Tensor out = make(q.sizes(), t, q);
         void* stream = here.stream();
@@ -284,6 +310,7 @@ PyObject* dequantize_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                     scale.numel() != 1, ptr(out), type_of(t), stream);
         }
         done(rc, "lecb_dequantize_q8");
+        if (grads) no_backward(name, {out}, scale);
         return THPVariable_Wrap(out);
     });
 }
@@ -312,6 +339,7 @@ PyObject* matvec_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         check(is_float(yt), yt, "matvec_w4: out_dtype");
         if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))
             refuse("matvec_w4: ws is contiguous uint8");
+        const bool grads = recorded(name, x, scales, xscale);
         const Here here(x, tiles, scales, xscale, ws);
         at::DimVector size(x.sizes());
         size.back() = n;
@@ -330,6 +358,7 @@ PyObject* matvec_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                 ptr(ws), ws.defined() ? ws.nbytes() : 0, stream);
         }
         done(rc, "lecb_matvec_w4");
+        if (grads) no_backward(name, {y}, x, scales, xscale);
         return THPVariable_Wrap(y);
     });
 }
@@ -346,6 +375,7 @@ PyObject* quantize_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         check(is_scale(st), st, "scale_dtype");
         if (group != 32 && group != 64 && group != 128) refuse("quantize_w4: group is 32, 64 or 128");
         const Rows wr(w, name);
+        recorded(name, w);   // codes and scales are constants to what follows
         const Here here(w);
         const int64_t nt = up(w.size(0), 16), kt = up(wr.cols, 128);
         const at::Tensor tiles = make({nt, kt, 1024}, at::kByte, w), scales = make({nt, kt * (128 / group), 16}, st, w);
@@ -371,6 +401,7 @@ PyObject* dequantize_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
         check_weights(tiles, scales, n, k, group);
         const at::ScalarType t = dtype(args[5], name);
         check(is_float(t), t, name);
+        const bool grads = recorded(name, scales);
         const Here here(tiles, scales);
         const at::Tensor out = make({n, k}, t, tiles);
         void* stream = here.stream();
@@ -381,6 +412,7 @@ PyObject* dequantize_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                     (uint32_t)group, n, k, ptr(out), type_of(t), k, stream);
         }
         done(rc, "lecb_dequantize_w4");
+        if (grads) no_backward(name, {out}, scales);
         return THPVariable_Wrap(out);
     });
 }

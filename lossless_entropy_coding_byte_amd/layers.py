@@ -118,7 +118,8 @@ class W4Weights:
 
 
 def quantize_w4(w, group: int = 128, scale_dtype=torch.bfloat16) -> W4Weights:
-    """Round a float matrix [n, k] to 4-bit codes with one scale per row and ``group`` columns."""
+    """Round a float matrix [n, k] to 4-bit codes with one scale per row and ``group`` columns.
+    No gradient goes back to w."""
     tiles, scales = _tensors.quantize_w4(w, group, scale_dtype)
     return W4Weights(tiles, scales, *w.shape, group)
 
@@ -156,7 +157,8 @@ def rmsnorm_q8(x, weight, residual=None, eps: float = 1e-6, scale=None, out_h=No
     [..., cols], scale float32 [...], h in x's type).  Without a residual h is
     x itself.  scale: a float32 tensor of one number fixes the scale for every
     row (values past it saturate) and is returned as given.  out_h: where h
-    goes; x or residual themselves will do."""
+    goes; x or residual themselves will do, other rows of theirs will not, nor
+    inputs that gradients are recorded for."""
     return _tensors.rmsnorm_q8(x, weight, residual, eps, scale, out_h)
 
 

@@ -95,3 +95,34 @@ def test_result_over_the_weight_or_the_scale():
         lecb.rmsnorm_q8(x, buf[96:128], residual=r, out_h=wide)
     with pytest.raises(ValueError, match="out_h overlaps"):
         lecb.rmsnorm_q8(x, buf[95:127], residual=r, out_h=wide)
+
+
+def test_tangents_are_refused():
+    """Forward-mode derivatives would be lost without a word."""
+    from torch.autograd import forward_ad as fw
+
+    def dual(t):
+        return fw.make_dual(t, torch.ones_like(t))
+
+    x, weight, r = torch.zeros(3, 128, dtype=BF16), torch.ones(128, dtype=BF16), torch.zeros(3, 128, dtype=BF16)
+    q, one = torch.zeros(3, 128, dtype=I8), torch.ones(1)
+    with fw.dual_level():
+        for call in (lambda: lecb.matvec_w4(dual(x), w4()), lambda: lecb.matvec_w4(q, w4(), x_scale=dual(one)),
+                     lambda: lecb.rmsnorm_q8(dual(x), weight), lambda: lecb.rmsnorm_q8(x, dual(weight)),
+                     lambda: lecb.rmsnorm_q8(x, weight, residual=dual(r)), lambda: lecb.dequantize_q8(q, dual(one)),
+                     lambda: lecb.quantize_w4(dual(x)),
+                     lambda: lecb.dequantize_w4(lecb.W4Weights(w4().tiles, dual(w4().scales), 16, 128))):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+
+
+def test_result_in_place_while_gradients_are_recorded():
+    """As torch's own out= arguments: with no derivative of what is written there."""
+    x, weight, r = torch.zeros(3, 128, dtype=BF16), torch.ones(128, dtype=BF16), torch.zeros(3, 128, dtype=BF16)
+    for which in range(3):
+        args = [t.clone().requires_grad_(i == which) for i, t in enumerate((x, weight, r))]
+        for out in (args[0], torch.empty_like(x)):
+            with pytest.raises(ValueError, match="gradients"):
+                lecb.rmsnorm_q8(args[0], args[1], residual=args[2], out_h=out)
+            with torch.no_grad(), pytest.raises(ValueError, match="current GPU"):
+                lecb.rmsnorm_q8(args[0], args[1], residual=args[2], out_h=out)
