@@ -280,6 +280,7 @@ PyObject* rmsnorm_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                  static_cast<int8_t*>(ptr(q)), static_cast<float*>(ptr(scale)), fixed, stream);
         }
         done(rc, "lecb_rmsnorm_q8");
+        if (given && !h.is_inference()) h.unsafeGetTensorImpl()->bump_version();   // for what autograd has kept of it
         if (grads) no_backward(name, {fixed ? at::Tensor() : scale, h}, x, weight, residual, scale);
         return tuple(THPVariable_Wrap(q), fixed ? share(args[4]) : THPVariable_Wrap(scale),
                      !residual.defined() ? share(args[0]) : given ? share(args[5]) : THPVariable_Wrap(h));

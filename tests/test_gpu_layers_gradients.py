@@ -67,3 +67,21 @@ def test_weights_are_constants():
     w, x, _, _ = _inputs()
     w4 = lecb.quantize_w4(torch.nn.Parameter(w))
     assert not w4.scales.requires_grad and not lecb.matvec_w4(x, w4, out_dtype=F32).requires_grad
+
+
+def test_h_in_place_is_seen_by_autograd():
+    """What a recorded product has kept is changed by a later call: its backward pass must not go on with it."""
+    _, x, r, weight = _inputs()
+    for kept in (x, r, torch.empty_like(x)):
+        kept.zero_()
+        before = kept._version
+        leaf = torch.ones_like(x).requires_grad_()
+        z = (leaf * kept).float().sum()
+        lecb.rmsnorm_q8(x, weight, residual=r, out_h=kept)
+        assert kept._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            z.backward()
+    with torch.inference_mode():
+        out = torch.empty_like(x)
+        assert lecb.rmsnorm_q8(x, weight, residual=r, out_h=out)[2] is out
+    assert lecb.rmsnorm_q8(x, weight, residual=r, out_h=out)[2] is out
