@@ -450,19 +450,32 @@ __global__ __launch_bounds__(256) void dequantize_q8_kernel(const int8_t* __rest
     if (total - at > 8) v[1].store(out + at + 8, total - at - 8);
 }
 
+// A launch has fewer than 2^32 lanes: more rows than that go by several.
+template <typename T, typename W, int THREADS, int NV>
+int launch_norm_rows(NormArgs a, hipStream_t s) {
+    constexpr uint32_t MOST = (1u << 31) / THREADS;
+    for (uint32_t left = a.rows; left;) {
+        const uint32_t rows = left < MOST ? left : MOST;
+        rmsnorm_q8_kernel<T, W, THREADS, NV><<<dim3(rows), THREADS, 0, s>>>(a);
+        const int rc = launched();
+        if (rc) return rc;
+        left -= rows;
+        a.x = static_cast<const T*>(a.x) + rows * a.x_stride;
+        if (a.res) a.res = static_cast<const T*>(a.res) + rows * a.res_stride;
+        if (a.h) a.h = static_cast<T*>(a.h) + rows * a.h_stride;
+        a.q += (uint64_t)rows * a.cols;
+        if (!a.static_scale) a.scale += rows;
+    }
+    return LECB_OK;
+}
+
 template <typename T, typename W>
 int launch_norm_as(const NormArgs& a, hipStream_t s) {
-    const dim3 grid(a.rows);
     const uint32_t pieces = (a.cols + 7) / 8;
-    if (pieces <= 64)
-        rmsnorm_q8_kernel<T, W, 64, 1><<<grid, 64, 0, s>>>(a);
-    else if (pieces <= 256)
-        rmsnorm_q8_kernel<T, W, 256, 1><<<grid, 256, 0, s>>>(a);
-    else if (pieces <= 1024)
-        rmsnorm_q8_kernel<T, W, 256, 4><<<grid, 256, 0, s>>>(a);
-    else
-        rmsnorm_q8_kernel<T, W, 1024, 4><<<grid, 1024, 0, s>>>(a);
-    return launched();
+    if (pieces <= 64) return launch_norm_rows<T, W, 64, 1>(a, s);
+    if (pieces <= 256) return launch_norm_rows<T, W, 256, 1>(a, s);
+    if (pieces <= 1024) return launch_norm_rows<T, W, 256, 4>(a, s);
+    return launch_norm_rows<T, W, 1024, 4>(a, s);
 }
 
 }  // namespace
