@@ -478,67 +478,78 @@ int launch_norm_as(const NormArgs& a, hipStream_t s) {
     return launch_norm_rows<T, W, 1024, 4>(a, s);
 }
 
+// Rows of 4-bit weights that one launch takes, a wave a tile: it has fewer than
+// 2^32 lanes.
+struct Share {
+    uint64_t row, rows, first_tile;
+    uint32_t kt, tiles;
+    dim3 grid() const { return dim3((tiles + 3) / 4); }
+};
+template <typename F>
+int by_rows(uint64_t n, uint64_t k, F launch) {
+    const uint64_t kt = tiles_of(k, TILE_COLS), most = (1ull << 25) / kt * TILE_ROWS;   // kt: 2^24 at most
+    for (uint64_t row = 0; row < n; row += most) {
+        const uint64_t rows = n - row < most ? n - row : most;
+        launch(Share{row, rows, row / TILE_ROWS * kt, (uint32_t)kt, (uint32_t)(tiles_of(rows, TILE_ROWS) * kt)});
+        const int rc = launched();
+        if (rc) return rc;
+    }
+    return LECB_OK;
+}
+
 }  // namespace
 
 int launch_quantize_w4(const QuantizeW4& a, void* stream) {
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const uint64_t kt = tiles_of(a.k, TILE_COLS), tiles = tiles_of(a.n, TILE_ROWS) * kt;
-    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
-    const dim3 grid((uint32_t)((tiles + 3) / 4));
-    const int bf16 = a.scale_type == LECB_BF16;
     return with_float_type(a.type, [&](auto t) -> int {
         typedef decltype(t) T;
         auto go = [&](auto group) {
             constexpr int G = decltype(group)::value;
-            quantize_w4_kernel<T, G><<<grid, 256, 0, s>>>(static_cast<const T*>(a.w), a.stride, a.n, a.k, (uint32_t)kt, (uint32_t)tiles,
-                                        reinterpret_cast<u32x4*>(a.tiles), a.scales, bf16);
+            return by_rows(a.n, a.k, [&](const Share& p) {
+                const uint64_t at = p.first_tile * (128 / G * TILE_ROWS) * (a.scale_type == LECB_BF16 ? 2 : 4);
+                quantize_w4_kernel<T, G><<<p.grid(), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+                    static_cast<const T*>(a.w) + p.row * a.stride, a.stride, p.rows, a.k, p.kt, p.tiles,
+                    reinterpret_cast<u32x4*>(a.tiles) + p.first_tile * 64, static_cast<char*>(a.scales) + at,
+                    a.scale_type == LECB_BF16);
+            });
         };
-        if (a.group == 32)
-            go(std::integral_constant<int, 32>());
-        else if (a.group == 64)
-            go(std::integral_constant<int, 64>());
-        else
-            go(std::integral_constant<int, 128>());
-        return launched();
+        if (a.group == 32) return go(std::integral_constant<int, 32>());
+        if (a.group == 64) return go(std::integral_constant<int, 64>());
+        return go(std::integral_constant<int, 128>());
     });
 }
 
 int launch_dequantize_w4(const DequantizeW4& a, void* stream) {
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const uint64_t kt = tiles_of(a.k, TILE_COLS), tiles = tiles_of(a.n, TILE_ROWS) * kt;
-    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
-    const dim3 grid((uint32_t)((tiles + 3) / 4));
     return with_float_type(a.type, [&](auto t) -> int {
         typedef decltype(t) T;
         auto go = [&](auto group) {
-            dequantize_w4_kernel<T, decltype(group)::value><<<grid, 256, 0, s>>>(
-                reinterpret_cast<const u32x4*>(a.tiles), a.scales, a.scale_type == LECB_BF16, a.n, a.k, (uint32_t)kt,
-                (uint32_t)tiles, static_cast<T*>(a.out), a.stride);
+            constexpr int G = decltype(group)::value;
+            return by_rows(a.n, a.k, [&](const Share& p) {
+                const uint64_t at = p.first_tile * (128 / G * TILE_ROWS) * (a.scale_type == LECB_BF16 ? 2 : 4);
+                dequantize_w4_kernel<T, G><<<p.grid(), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+                    reinterpret_cast<const u32x4*>(a.tiles) + p.first_tile * 64,
+                    static_cast<const char*>(a.scales) + at, a.scale_type == LECB_BF16, p.rows, a.k, p.kt, p.tiles,
+                    static_cast<T*>(a.out) + p.row * a.stride, a.stride);
+            });
         };
-        if (a.group == 32)
-            go(std::integral_constant<int, 32>());
-        else if (a.group == 64)
-            go(std::integral_constant<int, 64>());
-        else
-            go(std::integral_constant<int, 128>());
-        return launched();
+        if (a.group == 32) return go(std::integral_constant<int, 32>());
+        if (a.group == 64) return go(std::integral_constant<int, 64>());
+        return go(std::integral_constant<int, 128>());
     });
 }
 
-int launch_tile_w4(const uint8_t* rows, uint8_t* tiles_out, uint64_t n, uint64_t k, void* stream) {
-    const uint64_t kt = tiles_of(k, TILE_COLS), tiles = tiles_of(n, TILE_ROWS) * kt;
-    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
-    tile_w4_kernel<<<dim3((uint32_t)((tiles + 3) / 4)), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
-        rows, reinterpret_cast<u32x4*>(tiles_out), n, k, (uint32_t)kt, (uint32_t)tiles);
-    return launched();
+int launch_tile_w4(const uint8_t* rows, uint8_t* tiles, uint64_t n, uint64_t k, void* stream) {
+    return by_rows(n, k, [&](const Share& p) {
+        tile_w4_kernel<<<p.grid(), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+            rows + p.row * ((k + 1) / 2), reinterpret_cast<u32x4*>(tiles) + p.first_tile * 64, p.rows, k, p.kt, p.tiles);
+    });
 }
 
-int launch_untile_w4(const uint8_t* tiles_in, uint8_t* rows, uint64_t n, uint64_t k, void* stream) {
-    const uint64_t kt = tiles_of(k, TILE_COLS), tiles = tiles_of(n, TILE_ROWS) * kt;
-    if (tiles >= (1ull << 32)) return LECB_ERR_TOO_LARGE;
-    untile_w4_kernel<<<dim3((uint32_t)((tiles + 3) / 4)), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
-        reinterpret_cast<const u32x4*>(tiles_in), rows, n, k, (uint32_t)kt, (uint32_t)tiles);
-    return launched();
+int launch_untile_w4(const uint8_t* tiles, uint8_t* rows, uint64_t n, uint64_t k, void* stream) {
+    return by_rows(n, k, [&](const Share& p) {
+        untile_w4_kernel<<<p.grid(), 256, 0, reinterpret_cast<hipStream_t>(stream)>>>(
+            reinterpret_cast<const u32x4*>(tiles) + p.first_tile * 64, rows + p.row * ((k + 1) / 2), p.rows, k, p.kt,
+            p.tiles);
+    });
 }
 
 int launch_rmsnorm_q8(const RmsnormQ8& a, void* stream) {

@@ -40,3 +40,21 @@ def test_norm_of_many_rows(rows, cols, part):
         assert torch.equal(qf[p], lecb.rmsnorm_q8(x[p], w, scale=fixed)[0]), at
     got = lecb.rmsnorm_q8(x, w, residual=r, out_h=x)
     assert got[2] is x and torch.equal(x, h) and torch.equal(got[0], q) and torch.equal(got[1], s)
+
+
+def test_weights_of_many_tiles():
+    """2^26 tiles and some: rows of one column, so that only the tiles are long."""
+    need(160)
+    n, k, part = (1 << 30) + 21, 1, 1 << 24
+    w = torch.randn(n, k, dtype=BF16, device=DEV, generator=seeded(1))
+    w4 = lecb.quantize_w4(w)
+    values = lecb.dequantize_w4(w4)
+    codes = lecb.untile_w4(w4.tiles, n, k)
+    tiles = lecb.tile_w4(codes, n, k)
+    for at in range(0, n, part):
+        rows, cells = slice(at, at + part), slice(at // 16, (at + part) // 16)
+        want = lecb.quantize_w4(w[rows])
+        assert torch.equal(w4.tiles[cells], want.tiles) and torch.equal(w4.scales[cells], want.scales), at
+        assert torch.equal(values[rows], lecb.dequantize_w4(want)), at
+        assert torch.equal(codes[rows], lecb.untile_w4(want.tiles, want.n, k)), at
+        assert torch.equal(tiles[cells], want.tiles), at
