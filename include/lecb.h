@@ -619,8 +619,8 @@ int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const fl
  * BF16 x: scales of 2^118 and more are infinite.
  * The result does not depend on what else runs, and a token's row not on the
  * other rows' values.
- * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken); its
- * contents do not matter before or after.  m 0 does nothing.
+ * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken; may be more
+ * than a call comes to use); its contents do not matter before or after.  m 0 does nothing.
  * Errors: INVALID_ARG, WORKSPACE, TOO_LARGE (m >= 2^31). */
 uint64_t lecb_matvec_w4_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
 int lecb_matvec_w4(const void* d_x, int x_type, uint64_t x_stride, const float* d_xscale,

@@ -19,12 +19,12 @@ namespace {
 // order and sums of the tokens made once instead of by every workgroup.  Bound by
 // latency: 512 x 8192 bf16 6 us, 32 x 8192 int8 2.6 us.
 template <typename X, bool MANY>
-__global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t across) {
+__global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t first, uint32_t across) {
     typedef Operand<X> O;
     typedef Tokens<X> T;
     constexpr int TILES = 16 / T::UNITS;
     __shared__ u32x4 sh[256];
-    const uint32_t mt = blockIdx.x / across, tk0 = blockIdx.x % across * TILES;
+    const uint32_t mt = blockIdx.x / across, tk0 = (first + blockIdx.x % across) * TILES;
     const uint32_t unit = threadIdx.x % T::UNITS, sub = threadIdx.x / T::UNITS % TILES;
     const uint32_t token = threadIdx.x / 16, tk = tk0 + sub;
     const uint64_t t = (uint64_t)mt * 16 + token, col = (uint64_t)tk * TILE_COLS;
@@ -278,7 +278,6 @@ int launch_group(const MatvecArgs& a, hipStream_t s) {
     auto go = [&](auto wn) -> int {
         constexpr int WN = decltype(wn)::value;
         const uint64_t b = mblocks * tiles_of(a.nt, 4 * WN);
-        if (b >= 1u << 31) return LECB_ERR_TOO_LARGE;
         matmul_w4_kernel<X, S, GROUP, WN>
             <<<dim3((uint32_t)(b + 7) / 8 * 8), 64 * MM_WAVES, 0, s>>>(a, (uint32_t)mblocks, (uint32_t)b);
         return launched();
@@ -301,13 +300,18 @@ int launch_as(const MatvecArgs& a, int scale_type, uint32_t group, hipStream_t s
 template <typename X>
 int lay_as(const MatvecArgs& a, bool many, hipStream_t s) {
     const uint64_t across = tiles_of(a.kt, 16 / Tokens<X>::UNITS);
-    const uint64_t blocks = across * (many ? tiles_of(a.m, LAID_TOKENS) * (LAID_TOKENS / 16) : tiles_of(a.m, 16));
-    if (blocks >= 1u << 31) return LECB_ERR_TOO_LARGE;
-    if (many)
-        lay_tokens_kernel<X, true><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, (uint32_t)across);
-    else
-        lay_tokens_kernel<X, false><<<dim3((uint32_t)blocks), 256, 0, s>>>(a, (uint32_t)across);
-    return launched();
+    const uint64_t down = many ? tiles_of(a.m, LAID_TOKENS) * (LAID_TOKENS / 16) : tiles_of(a.m, 16);
+    for (uint64_t first = 0; first < across; first += LAY_ACROSS) {
+        const uint32_t here = (uint32_t)(across - first < LAY_ACROSS ? across - first : LAY_ACROSS);
+        const dim3 grid((uint32_t)(here * down));
+        if (many)
+            lay_tokens_kernel<X, true><<<grid, 256, 0, s>>>(a, (uint32_t)first, here);
+        else
+            lay_tokens_kernel<X, false><<<grid, 256, 0, s>>>(a, (uint32_t)first, here);
+        const int rc = launched();
+        if (rc) return rc;
+    }
+    return LECB_OK;
 }
 
 }  // namespace

@@ -362,14 +362,12 @@ __global__ __launch_bounds__(64) void add_parts_kernel(MatvecArgs a) {
 
 template <typename X, typename S, int GROUP, int MT, int NT, int ROWS>
 int launch_few(const MatvecArgs& a, hipStream_t s) {
-    const uint64_t mt = tiles_of(a.m, 16 * MT);
-    if (mt > 65535) return LECB_ERR_TOO_LARGE;
     // No more waves than have DEPTH tiles each, but four: what a wave asks for past
     // its last tile costs loads, a wave more only a share of the last sums.
     uint32_t waves = few_waves(MT, NT);
     while (waves > 4 && waves * few_depth(MT, NT) > tiles_of(a.kt, a.splits)) waves /= 2;
     matvec_w4_kernel<X, S, GROUP, MT, NT, ROWS>
-        <<<dim3((uint32_t)tiles_of(a.nt, NT), (uint32_t)mt, a.splits), waves * 64, 0, s>>>(a);
+        <<<dim3((uint32_t)tiles_of(a.nt, NT), (uint32_t)tiles_of(a.m, 16 * MT), a.splits), waves * 64, 0, s>>>(a);
     if (a.splits > 1)
         add_parts_kernel<<<dim3((uint32_t)tiles_of(a.m * a.nt, 16)), 64, 0, s>>>(a);
     return launched();
@@ -449,21 +447,34 @@ bool many(const MatvecArgs& a) {
     return 3 * rounds > 2 * matmul_w4_turns(a);
 }
 
-}  // namespace
-
-namespace {
-uint64_t laying_bytes(uint64_t m, uint64_t kt) {   // what no address needs is not asked for
+// Asked for whatever the tokens' addresses are; 9 to 16 tokens of short rows are
+// asked for it too, though they go by in_rows.
+uint64_t laying_bytes(uint64_t m, uint64_t kt) {
     return m <= 4 || (m <= 8 && kt <= 16) ? 0 : laid_bytes(m, kt);
 }
-}  // namespace
-
-uint64_t matvec_w4_workspace(uint64_t m, uint64_t n, uint64_t k) {
+uint64_t bytes_of(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t kt = tiles_of(k, TILE_COLS);
-    return m ? laying_bytes(m, kt) + parts_bytes(m, tiles_of(n, TILE_ROWS), kt) : 0;
+    return m && n ? laying_bytes(m, kt) + parts_bytes(m, tiles_of(n, TILE_ROWS), kt) : 0;
 }
 
-int launch_matvec_w4(const MatvecW4& m, void* stream) {
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+// What one pass of launches takes; more tokens and rows go by several passes, one
+// after another with the same workspace.  A grid has fewer than 2^32 lanes and
+// 65536 workgroups along y: 64 tokens a workgroup of few tokens; of many, 512 lanes
+// for 64 tokens x 16 tiles of rows or more; of laying out, 256 lanes for 16 tokens
+// x one tile of columns or more (up to LAY_ACROSS, as launch_lay_tokens has it).
+struct Pass {
+    uint64_t tokens, rows;
+};
+Pass pass_of(uint64_t n, uint64_t k) {
+    constexpr uint64_t ROW_TILES = 1u << 22;
+    const uint64_t nt = tiles_of(n, TILE_ROWS), kt = tiles_of(k, TILE_COLS);
+    const uint64_t products = (1u << 22) / tiles_of(nt < ROW_TILES ? nt : ROW_TILES, 16);
+    const uint64_t laying = LAY_ACROSS / (kt < LAY_ACROSS ? kt : LAY_ACROSS);
+    const uint64_t blocks = products < laying ? products : laying;
+    return {LAID_TOKENS * (blocks < 65535 ? blocks : 65535), ROW_TILES * TILE_ROWS};
+}
+
+int launch_pass(const MatvecW4& m, hipStream_t s) {
     const uint64_t nt = tiles_of(m.n, TILE_ROWS), kt = tiles_of(m.k, TILE_COLS);
     const MatvecArgs a{m.x, m.xscale, reinterpret_cast<const u32x4*>(m.tiles), m.scales, m.y, m.ws, m.x_stride,
                        m.y_stride, m.n, m.k, m.m, (uint32_t)nt, (uint32_t)kt, m.xscale_stride, m.y_type,
@@ -481,6 +492,38 @@ int launch_matvec_w4(const MatvecW4& m, void* stream) {
         case LECB_BF16: return launch_as<__bf16>(a, rows, m.scale_type, m.group, s);
         default: return launch_as<_Float16>(a, rows, m.scale_type, m.group, s);
     }
+}
+
+}  // namespace
+
+uint64_t matvec_w4_workspace(uint64_t m, uint64_t n, uint64_t k) {
+    const Pass p = pass_of(n, k);
+    uint64_t most = 0;
+    for (const uint64_t tokens : {m < p.tokens ? m : p.tokens, m % p.tokens})
+        for (const uint64_t rows : {n < p.rows ? n : p.rows, n % p.rows}) {
+            const uint64_t b = bytes_of(tokens, rows, k);
+            most = b > most ? b : most;
+        }
+    return most;
+}
+
+int launch_matvec_w4(const MatvecW4& m, void* stream) {
+    const Pass p = pass_of(m.n, m.k);
+    const uint64_t kt = tiles_of(m.k, TILE_COLS), scales = TILE_COLS / m.group * TILE_ROWS * elem_bytes(m.scale_type);
+    for (uint64_t token = 0; token < m.m; token += p.tokens)
+        for (uint64_t row = 0; row < m.n; row += p.rows) {
+            MatvecW4 one = m;
+            one.m = m.m - token < p.tokens ? m.m - token : p.tokens;
+            one.n = m.n - row < p.rows ? m.n - row : p.rows;
+            one.x = static_cast<const char*>(m.x) + token * m.x_stride * elem_bytes(m.x_type);
+            if (m.xscale) one.xscale = m.xscale + token * m.xscale_stride;
+            one.tiles = m.tiles + row / TILE_ROWS * kt * TILE_BYTES;
+            one.scales = static_cast<const char*>(m.scales) + row / TILE_ROWS * kt * scales;
+            one.y = static_cast<char*>(m.y) + (token * m.y_stride + row) * elem_bytes(m.y_type);
+            const int rc = launch_pass(one, reinterpret_cast<hipStream_t>(stream));
+            if (rc) return rc;
+        }
+    return LECB_OK;
 }
 
 }  // namespace lecb

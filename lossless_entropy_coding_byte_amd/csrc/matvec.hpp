@@ -261,6 +261,7 @@ __host__ __device__ inline uint64_t laid_units(uint64_t m, uint64_t kt, uint64_t
 inline uint64_t laid_bytes(uint64_t m, uint64_t kt) { return laid_units(m, kt, 2) * 16; }   // of the widest type
 inline __device__ const u32x4* laid_tokens(const MatvecArgs& a) { return reinterpret_cast<const u32x4*>(a.ws); }
 
+constexpr uint64_t LAY_ACROSS = 1u << 21;   // workgroups along the columns of one launch
 int launch_lay_tokens(const MatvecArgs& a, int x_type, bool many, hipStream_t s);
 constexpr uint32_t MM_TILES = 1u << 22;   // more tiles of columns than this: in the form for few tokens
 uint64_t matmul_w4_turns(const MatvecArgs& a);   // its time, in 64 x 64 outputs of a wave

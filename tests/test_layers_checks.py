@@ -126,3 +126,17 @@ def test_result_in_place_while_gradients_are_recorded():
                 lecb.rmsnorm_q8(args[0], args[1], residual=args[2], out_h=out)
             with torch.no_grad(), pytest.raises(ValueError, match="current GPU"):
                 lecb.rmsnorm_q8(args[0], args[1], residual=args[2], out_h=out)
+
+
+def test_workspace_of_many_tokens_and_rows():
+    """Tokens and rows past what one pass of launches takes share its workspace."""
+    ask = lecb.lecb_matvec_w4_workspace_bytes
+    most = 65535 * 64
+    assert ask(most, 64, 128) == most * 128 * 2
+    for m in (most + 1, 2 * most, (1 << 31) - 1):
+        assert ask(m, 64, 128) == ask(most, 64, 128)
+    assert ask(100, (1 << 31) - 1, 128) == ask(100, 1 << 26, 128) >= 128 * 128 * 2
+    # a workspace for the most tokens serves fewer
+    for n, k in ((16, 28672), (1000, 8192), (8192, 8192), (64, 128)):
+        sizes = [ask(m, n, k) for m in (1, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 512, 10000)]
+        assert sizes == sorted(sizes)
