@@ -498,6 +498,7 @@ int launch_pass(const MatvecW4& m, hipStream_t s) {
 
 uint64_t matvec_w4_workspace(uint64_t m, uint64_t n, uint64_t k) {
     const Pass p = pass_of(n, k);
+    if (m <= p.tokens && n <= p.rows) return bytes_of(m, n, k);
     uint64_t most = 0;
     for (const uint64_t tokens : {m < p.tokens ? m : p.tokens, m % p.tokens})
         for (const uint64_t rows : {n < p.rows ? n : p.rows, n % p.rows}) {
