@@ -15,9 +15,9 @@ namespace {
 //
 // What the products gain from it: whole, aligned loads of 1 KiB where rows of a
 // power of two bytes apart would come from one memory channel, sixteen at a time
-// (32 x 8192 x 8192 int8: 19 us without, 12.6 with), no partial tiles, and the
-// order and sums of the tokens made once instead of by every workgroup.  Bound by
-// latency: 512 x 8192 bf16 6 us, 32 x 8192 int8 2.6 us.
+// (32 x 8192 x 8192 int8: 19 us without, 12.8 with), no partial tiles, and the
+// order of the tokens made once instead of by every workgroup.  Bound by latency:
+// 512 x 8192 bf16 6 us, 32 x 8192 int8 2.7 us.
 template <typename X, bool MANY>
 __global__ __launch_bounds__(256) void lay_tokens_kernel(MatvecArgs a, uint32_t first, uint32_t across) {
     typedef Operand<X> O;
@@ -78,14 +78,15 @@ __device__ __forceinline__ void mm_step(const Tile* __restrict__ now, Tile* __re
 //
 // Bound by that issue: of 16-bit tokens, a tile of 128 columns costs a wave 32
 // matrix instructions (1024 cycles), about 280 vector ones (208 for its words,
-// 64 a group for the scales) and 90 others.  512 x 8192 x 8192 with the layout of
-// the tokens, bf16: groups of 128 80 us, of 64 81, of 32 94; operands with an
-// offset (Operand), which eight instructions a word make instead of 13 but whose
-// sums are read from LDS for every group: 77, 88 and 99.  int8, groups of 128, 51 us (the
-// library's product of two bf16 matrices of 8192 x 8192: 1250 TFLOP/s).  Tried
-// and slower: one matrix instruction, then a share of the vector ones, in turn
-// (+ 15 %, as then neither wave of a SIMD runs ahead); all words' numbers before
-// all products (registers); a wave's words through LDS (its reads are the bound).
+// 64 a group for the scales) and 90 others.  512 x 8192 x 8192 bf16: groups of 128
+// 70 us, 980 TFLOP/s, of 64 75, of 32 86; int8, groups of 128, 46 us.  With the layout
+// of the tokens, on a slower card: 80, 81 and 94; operands with an offset (Operand),
+// which eight instructions a word make instead of 13 but whose sums are read from
+// LDS for every group, 77, 88 and 99 there (the library's product of two bf16
+// matrices of 8192 x 8192: 1250 TFLOP/s).  Tried and slower: one matrix
+// instruction, then a share of the vector ones, in turn (+ 15 %, as then neither
+// wave of a SIMD runs ahead); all words' numbers before all products (registers);
+// a wave's words through LDS (its reads are the bound).
 template <typename X, typename S, int GROUP, int WN>
 __global__ __launch_bounds__(64 * MM_WAVES) void matmul_w4_kernel(MatvecArgs a, uint32_t mblocks, uint32_t blocks) {
     typedef Operand<X> O;

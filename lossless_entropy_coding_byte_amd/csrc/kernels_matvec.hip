@@ -208,11 +208,13 @@ struct InRows {
 // few rows of W and many columns, several workgroups share the columns of a block
 // (blockIdx.z); add_parts_kernel adds their sums up.
 //
-// One token: bound by HBM where W is large (28672 x 8192 bf16 25 us, 4.8 TB/s; W
-// is read once and does not stay in the cache) and by latency where it is not
-// (4096 x 4096 int8 4.1 us).  More tokens: by loads, of which a tile takes
-// PIECES MT + NT + 1 or more (32 x 8192 x 8192 int8 10.5 us, 64 x 8192 x 8192
-// bf16 21 us).
+// One token: bound by HBM where W is large (28672 x 8192: int8 25 us, 4.8 TB/s; bf16
+// 28 us, as making operands of the words that come last is not hidden; W is read
+// once and does not stay in the cache) and by latency where it is not (4096 x 4096
+// int8 4.2 us).  More tokens: by loads, of which a tile takes PIECES MT + NT + 1 or
+// more (8192 x 8192: 32 tokens int8 11 us, bf16 14; 64 tokens int8 14, bf16 18).
+// One token with three tiles in flight, 16 waves or two tiles of rows instead of
+// four: 31, 33 and 29 us where this took 29.
 template <typename X, typename S, int GROUP, int MT, int NT, int ROWS>
 __global__ __launch_bounds__(64 * few_waves(MT, NT)) void matvec_w4_kernel(MatvecArgs a) {
     typedef Operand<X> O;
@@ -409,12 +411,13 @@ int launch_as(const MatvecArgs& a, bool rows, int scale_type, uint32_t group, hi
 }
 
 // Whether tokens are read from their rows, without a launch to lay them out
-// first (2.6 us, and as much of the host: 5 x 1003 x 1111 takes 9.6 us so, 5.5 in
-// rows): always up to four, and up to 16 where rows are short; up to 16 too where
-// their loads are aligned and, above eight, rows not too long.  8192 x 8192 bf16,
-// in rows and laid out, us: 8 tokens 10.2 and 13.5, 16 tokens 14 and 13.7; 8
-// tokens of 8191 columns 19.3 and 13.4; 1000 x 28672, 16 tokens, 34 and 25.  Both
-// give the same bits: the same instructions on the same operands, in the same order.
+// first (2.7 us, and as much of the host): always up to four, and up to 16 where
+// rows are short; up to 16 too where their loads are aligned and, above eight, rows
+// not too long.  In rows and laid out, us, in a graph: 5 x 1003 x 1111 bf16 5.2 and
+// 6.3; 8192 x 8192 bf16, 8 tokens 10.5 and 14.2, 16 tokens 13.8 and 14.3; 8 tokens
+// of 8191 columns 19.3 and 13.7; 1000 x 28672, 16 tokens, int8 14.2 and 13.2, bf16
+// 14.9 and 15.3, of 28001 columns 28.0 and 15.4.  Both give the same bits: the same
+// instructions on the same operands, in the same order.
 bool in_rows(const MatvecArgs& a, uint64_t bytes) {
     if (a.m <= 4 || (a.m <= 16 && a.kt <= 16)) return true;
     const bool aligned = (reinterpret_cast<uintptr_t>(a.x) | a.x_stride * bytes) % (8 * bytes) == 0;
@@ -424,7 +427,8 @@ bool in_rows(const MatvecArgs& a, uint64_t bytes) {
 // Shares of the columns over workgroups: where the blocks of outputs (16 rows, up
 // to 64 tokens) leave half of the compute units or more idle and every share
 // keeps 32 tiles; up to four tokens, whose blocks are sooner done, from 128 tiles
-// on.  The sums' second launch takes 2 us.
+// on.  The sums' launch takes 2.5 us.  1000 x 28672 bf16 without and with shares, us,
+// in a graph: 1 token 12.2 and 9.5, 16 tokens 25.0 and 15.3, 64 tokens 56 and 25.
 uint64_t splits_of(uint64_t m, uint64_t nt, uint64_t kt) {
     const uint64_t blocks = nt * tiles_of(m, m <= 16 ? 16 : m <= 32 ? 32 : 64);
     const uint64_t idle = (uint64_t)device_cu_count() / blocks, most = kt / (m <= 4 ? 64 : 32);
@@ -438,8 +442,8 @@ uint64_t parts_bytes(uint64_t m, uint64_t nt, uint64_t kt) {
 
 // Whether the form for many tokens takes it.  A round of its workgroups (64 x 256
 // outputs a compute unit) takes about 8/3 as long as one here (64 x 32):
-// 8192 x 8192 bf16, 65 to 128 tokens, 40 us here and 57 there; 300 tokens, 98 and
-// 60; 28672 x 4096, 48 tokens, 42 and 35; 1024 x 8192, 512 tokens, 26 and 60.
+// 8192 x 8192 bf16, 65 to 128 tokens, 36 to 40 us here and 62 there; 300 tokens, 92
+// and 63; 28672 x 4096, 48 tokens, 42 and 37; 1024 x 8192, 512 tokens, 25 and 62.
 bool many(const MatvecArgs& a) {
     if (a.m <= 32 || a.kt >= MM_TILES) return false;
     const uint64_t cus = (uint64_t)device_cu_count();

@@ -163,7 +163,8 @@ def rmsnorm_q8(x, weight, residual=None, eps: float = 1e-6, scale=None, out_h=No
 
 
 def dequantize_q8(q, scale, dtype=torch.bfloat16):
-    """The values q * scale of int8 codes [..., cols]; scale: one float32 per row, or one."""
+    """The values q * scale of int8 codes [..., cols]; scale: one float32 per row, or one.
+    q is contiguous and 16-byte aligned (as rmsnorm_q8 returns it; rows of it may not be)."""
     return _tensors.dequantize_q8(q, scale, dtype)
 
 
