@@ -590,8 +590,8 @@ int lecb_untile_w4(const uint8_t* d_tiles, uint64_t n, uint64_t k, uint8_t* d_ro
  *   float that is read and used for every row (a scale fixed beforehand, as
  *   a fixed codebook is): q = y / scale saturates at -127 and 127.
  * A row with an infinity or NaN, or whose sum of squares overflows 32 bits (some
- * |h| above 2^63), gets scale = NaN and q = 0; a
- * row of zeros gets scale 0 and q = 0.  With static_scale, NaN gives q = 0 and
+ * |h| above 2^63), gets scale = NaN and q = 0; a row of zeros gets scale 0 and
+ * q = 0; one whose max|y| is past 32 bits gets an infinite scale.  With static_scale, NaN gives q = 0 and
  * so does a scale that is not above 0.
  * cols in 1..LECB_NORM_MAX_COLS, eps > 0 and finite.  rows 0 does nothing.
  * Errors: INVALID_ARG, TOO_LARGE (rows >= 2^31). */
@@ -616,7 +616,8 @@ int lecb_dequantize_q8(const int8_t* d_q, uint64_t rows, uint64_t cols, const fl
  * (2 group + groups + 24) 2^-24 of the sum of |x q s| before the last rounding;
  * a column whose code is 0 adds nothing to it, however large x is there.
  * Infinities and NaN in x do what the formula says (an infinity times 0 is NaN).
- * BF16 x: scales of 2^118 and more are infinite.
+ * BF16 x: scales of 2^118 and more are infinite.  I8 x: so are sums, before x's
+ * own scale, of 2^124 and more.
  * The result does not depend on what else runs, and a token's row not on the
  * other rows' values.
  * d_ws: lecb_matvec_w4_workspace_bytes (may be 0, then NULL is taken; may be more
