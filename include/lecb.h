@@ -629,6 +629,112 @@ int lecb_matvec_w4(const void* d_x, int x_type, uint64_t x_stride, const float* 
                    int scale_type, uint32_t group, uint64_t n, uint64_t k, void* d_y, int y_type,
                    uint64_t y_stride, void* d_ws, uint64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ 8-bit cache of keys and values
+ * What a decoder keeps of the tokens it has seen, in int8 blocks that the codec
+ * takes as bytes like any other, and the attention that reads them as they lie.
+ *
+ * A cache holds `blocks` blocks of `block` tokens (32, 64, 128 or 256).  Each
+ * block has, for every head, one scale for its keys and one for its values:
+ * x = q * scale.  Dimensions are padded with zero codes to P = 64, 96, 128, 192
+ * or 256, the first that is not below dim; codes stand in units of 32 tokens x
+ * 32 dimensions:
+ *   k, v    = i8 [blocks][heads][block/32][P/32][1024], 16-byte aligned;
+ *   k_scale, v_scale = f32 [blocks][heads];
+ *   unit of keys:   token t, dimension d of it at byte
+ *                   (((d % 32 / 8) * 16 + t % 16) * 2 + t / 16) * 8 + d % 8;
+ *   unit of values: ((((t % 16) / 4 * 16 + d % 16) * 2 + d / 16) * 2 + t / 16) * 4 + t % 4
+ * (t, d counted from the unit's own first): lane 16 g + r of a wave reads its 16
+ * bytes in one load, and either half of them is its part of a matrix operand.
+ *
+ * The sequences of a call: sequence s's tokens i * block and on stand in block
+ * table[s * table_stride + i] of the cache.  `lengths` counts a sequence's
+ * tokens, its rows of this call (starts[s] .. starts[s + 1] of the call's
+ * `tokens` rows; starts NULL: row s alone) being the last of them.  starts
+ * rises; sequences may have no rows; rows before the first and behind the last
+ * sequence belong to none.  All three arrays are read on the device alone, so that
+ * a captured call follows what they hold: entries that fit nothing can not be
+ * refused and lead to no access out of bounds, but to what each entry states. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    uint64_t blocks;   /* below 2^31 */
+    uint32_t heads;    /* 1..65535 */
+    uint32_t dim;      /* 1..256 */
+    uint32_t block;
+} lecb_cache_q8;
+
+typedef struct {
+    const int32_t* table;     /* [seqs][width], rows table_stride apart */
+    const int32_t* lengths;   /* [seqs] */
+    const int32_t* starts;    /* [seqs + 1] or NULL (then tokens = seqs) */
+    uint64_t table_stride;
+    uint32_t width;           /* width * block below 2^31 */
+    uint32_t seqs;            /* below 2^20 */
+    uint32_t tokens;          /* below 2^27 */
+} lecb_cache_seqs;
+
+/* Bytes of the codes of a cache's keys (its values take as many).  0 on bad arguments. */
+uint64_t lecb_cache_q8_bytes(uint64_t blocks, uint32_t heads, uint32_t dim, uint32_t block);
+
+/* Quantises the rows' keys and values (type F32, BF16 or F16; element (row, head,
+ * i) at row * token stride + head * head stride + i) into the cache.  For the new
+ * tokens of one block and head, need = max|x| / 127, rounded to 32 bits.
+ *   A block that holds older tokens of the sequence keeps its scale if need is not above it;
+ *   else scale = max(need, 1.25 * its scale), and the older codes are rounded
+ *   again, q * old scale / scale.  (Growing by a quarter at least keeps what
+ *   repeated roundings add up to below 2.5 steps.)
+ *   A block without older tokens gets scale = need.
+ * q = x / scale rounded to nearest (the exact quotient decides, half a step goes
+ * to the even code) in -127..127; 0 where scale is 0.  An infinity or NaN among
+ * the new tokens, or a scale that is NaN already, makes scale NaN and the block's
+ * codes for this head 0.
+ * Codes past a sequence's length mean nothing.  The blocks that a call writes must
+ * belong to one sequence each.  Tokens whose block is not one of the cache's, or of a
+ * sequence whose length exceeds width * block, are left out.
+ * Errors: INVALID_ARG, TOO_LARGE (what the structs' comments bound). */
+int lecb_cache_write_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, const void* d_k, const void* d_v,
+                        int type, uint64_t k_token_stride, uint64_t k_head_stride, uint64_t v_token_stride,
+                        uint64_t v_head_stride, void* stream);
+
+/* The rows' keys and values as the cache holds them: q * scale, a product in 32
+ * bits, rounded to `type`, to d_k and d_v [tokens][heads][dim].  The rows of a
+ * sequence are its last tokens, as in the other entries: starts that give each
+ * sequence as many rows as it has tokens read everything.  A row whose block
+ * is not one of the cache's, or of a sequence whose length exceeds width * block, is
+ * NaN; one of a sequence that has fewer tokens than rows, before its first, is 0.
+ * Rows of no sequence are set to 0 with fill = 1, left as they are with fill = 0.
+ * Errors: as above. */
+int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, void* d_k, void* d_v, int type,
+                       int fill, void* stream);
+
+/* Attention of the rows' queries over the cache:
+ *   out[i][h] = sum_j p_j v_j,  p = softmax_j(scale * q[i][h] . k_j),
+ * k_j and v_j of head h / (heads / cache heads), over the sequence's tokens j
+ * up to the row's own (causal = 1) or all of them (causal = 0); with a window
+ * (> 0, causal = 1 only) over the last `window` of these.  A row that sees
+ * nothing is 0.  q and out: type F32, BF16 or F16, element (row, head, i) at row *
+ * token stride + head * head stride + i; out must not overlap q.
+ * Codes are exact in the products, q to 2^-30 of its row's largest element, sums
+ * and the softmax have 32 bits; its weights enter the second product with 11
+ * bits (BF16 out) or 22.  Scales of values are told apart from 2^-60 up.
+ * A row with an infinity or NaN in q is NaN, and so is one that sees a
+ * block whose scale is NaN, a block that is not one of the cache's, or whose sequence's
+ * length exceeds width * block.  What a row does not see never matters.  Rows
+ * of no sequence: as in lecb_cache_read_q8.
+ * How the work is split, and with it the order of sums, depends on the lengths
+ * of all sequences; the same call gives the same bits.
+ * d_ws: lecb_attention_q8_workspace_bytes (may be 0, then NULL is taken); its
+ * contents do not matter before or after.
+ * Errors: INVALID_ARG, WORKSPACE, TOO_LARGE (also tokens * heads >= 2^31). */
+uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t seqs, uint32_t tokens,
+                                           uint32_t width, uint32_t heads);
+int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_stride, int type, uint32_t heads,
+                      const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, float scale, int causal,
+                      uint32_t window, void* d_out, uint64_t out_token_stride, uint64_t out_head_stride, int fill,
+                      void* d_ws, uint64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

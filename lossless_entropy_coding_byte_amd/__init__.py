@@ -8,8 +8,9 @@ and chain those calls.  If the library is not built this module raises on
 first use -- there is no fallback of any kind.
 
 The operators of quantised layers (``quantize_w4``, ``rmsnorm_q8``,
-``matvec_w4`` and what goes with them) are defined in ``layers.py``, which
-needs torch, and are reached as attributes of this package.
+``matvec_w4`` and what goes with them) are defined in ``layers.py``, those of the
+8-bit cache of keys and values in ``cache.py``, both of which
+need torch, and are reached as attributes of this package.
 """
 
 from __future__ import annotations
@@ -153,25 +154,37 @@ _SIGNATURES = {
     "lecb_matvec_w4_workspace_bytes": (_u64, [_u64, _u64, _u64]),
     "lecb_matvec_w4": (_int, [_vp, _int, _u64, _vp, _int, _u64, _vp, _vp, _int, _u32, _u64, _u64, _vp, _int, _u64,
                               _vp, _u64, _vp]),
+    "lecb_cache_q8_bytes": (_u64, [_u64, _u32, _u32, _u32]),
+    "lecb_cache_write_q8": (_int, [_vp, _vp, _vp, _vp, _int, _u64, _u64, _u64, _u64, _vp]),
+    "lecb_cache_read_q8": (_int, [_vp, _vp, _vp, _vp, _int, _int, _vp]),
+    "lecb_attention_q8_workspace_bytes": (_u64, [_vp, _u32, _u32, _u32, _u32]),
+    "lecb_attention_q8": (_int, [_vp, _u64, _u64, _int, _u32, _vp, _vp, ctypes.c_float, _int, _u32, _vp, _u64, _u64,
+                                 _int, _vp, _u64, _vp]),
 }
 
-# Names of layers.py that are this package's too (resolved on first use: importing
-# the codec's host functions alone does not import torch).
+# Names of layers.py and cache.py that are this package's too (resolved on first use:
+# importing the codec's host functions alone does not import torch).
 _LAYERS = (
     "W4Weights", "quantize_w4", "dequantize_w4", "tile_w4", "untile_w4", "rmsnorm_q8", "dequantize_q8", "matvec_w4",
     "lecb_w4_tile_bytes", "lecb_w4_scale_count", "lecb_matvec_w4_workspace_bytes", "lecb_quantize_w4",
     "lecb_dequantize_w4", "lecb_tile_w4", "lecb_untile_w4", "lecb_rmsnorm_q8", "lecb_dequantize_q8",
     "lecb_matvec_w4", "LECB_F32", "LECB_BF16", "LECB_F16", "LECB_I8", "NORM_MAX_COLS",
 )
+_CACHE = (
+    "CacheQ8", "new_cache_q8", "cache_write_q8", "cache_read_q8", "attention_q8", "lecb_cache_q8", "lecb_cache_seqs",
+    "lecb_cache_q8_bytes", "lecb_cache_write_q8", "lecb_cache_read_q8", "lecb_attention_q8_workspace_bytes",
+    "lecb_attention_q8",
+)
 
 
 def __getattr__(name):
-    if name not in _LAYERS:
+    if name not in _LAYERS and name not in _CACHE:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layers
+    from . import cache, layers
 
-    for n in _LAYERS:
-        globals()[n] = getattr(layers, n)
+    for module, names in ((layers, _LAYERS), (cache, _CACHE)):
+        for n in names:
+            globals()[n] = getattr(module, n)
     return globals()[name]
 
 

@@ -1,6 +1,6 @@
-// The operators of quantised layers on torch tensors: checks, results from
-// torch's allocator, one call of the C ABI each.  layers.py documents them and
-// is what users call.  On small tensors a call lasts as long as the host takes:
+// The operators of quantised layers and of the 8-bit cache on torch tensors: checks, results from
+// torch's allocator, one call of the C ABI each.  layers.py and cache.py document
+// them and are what users call.  On small tensors a call lasts as long as the host takes:
 // rmsnorm_q8 of one row 4.8 us here, 13 us with the same steps in Python and ctypes.
 #include <Python.h>
 
@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <memory>
 #include <string>
@@ -418,9 +419,219 @@ PyObject* dequantize_w4(PyObject*, PyObject* const* args, Py_ssize_t count) {
     });
 }
 
+// A cache as the kernels take it on trust: its fields may have been set since
+// CacheQ8 checked them.  args: k, v, k_scale, v_scale, dim, block.
+struct Cache {
+    at::Tensor k, v, k_scale, v_scale;
+    lecb_cache_q8 c;
+    explicit Cache(PyObject* const* args)
+        : k(tensor(args[0], "cache")), v(tensor(args[1], "cache")), k_scale(tensor(args[2], "cache")),
+          v_scale(tensor(args[3], "cache")) {
+        const int64_t dim = integer(args[4]), block = integer(args[5]);
+        if (dim < 1 || dim > 256 || (block != 32 && block != 64 && block != 128 && block != 256))
+            refuse("cache: dim is 1 to 256, block 32, 64, 128 or 256");
+        if (k_scale.dim() != 2 || k_scale.sizes() != v_scale.sizes() || k_scale.scalar_type() != at::kFloat ||
+            v_scale.scalar_type() != at::kFloat || !k_scale.is_contiguous() || !v_scale.is_contiguous())
+            refuse("cache: k_scale and v_scale are contiguous float32 [blocks, heads]");
+        const int64_t blocks = k_scale.size(0), heads = k_scale.size(1);
+        if (blocks < 1 || blocks >= int64_t(1) << 31 || heads < 1 || heads > 65535)
+            refuse("cache: 1 to 2^31 - 1 blocks and 1 to 65535 heads are needed");
+        const int64_t bytes = (int64_t)lecb_cache_q8_bytes(blocks, (uint32_t)heads, (uint32_t)dim, (uint32_t)block);
+        for (const at::Tensor& t : {k, v})
+            if (t.scalar_type() != at::kChar || t.numel() != bytes || !t.is_contiguous())
+                refuse("cache: k and v are " + std::to_string(bytes) + " contiguous int8 codes for these blocks, heads and dim");
+        c = {ptr(k), ptr(v), static_cast<float*>(ptr(k_scale)), static_cast<float*>(ptr(v_scale)), (uint64_t)blocks,
+             (uint32_t)heads, (uint32_t)dim, (uint32_t)block};
+    }
+};
+
+// The sequences of a call.  args: table, lengths, starts or None.
+struct Sequences {
+    at::Tensor table, lengths, starts;
+    lecb_cache_seqs s;
+    Sequences(PyObject* const* args, const Cache& cache, int64_t tokens, const std::string& name)
+        : table(tensor(args[0], "table")), lengths(tensor(args[1], "lengths")), starts(optional(args[2], "starts")) {
+        const int64_t seqs = lengths.dim() == 1 ? lengths.size(0) : -1;
+        if (seqs < 1 || lengths.scalar_type() != at::kInt || !lengths.is_contiguous())
+            refuse(name + ": lengths are contiguous int32, one for each sequence, at least one");
+        if (table.dim() != 2 || table.size(0) != seqs || table.scalar_type() != at::kInt || table.size(1) < 1 ||
+            (table.size(1) > 1 && table.stride(1) != 1) || (seqs > 1 && table.stride(0) < table.size(1)))
+            refuse(name + ": table is int32 [sequences, blocks], rows contiguous and apart, at least one block wide");
+        if (starts.defined()) {
+            if (starts.dim() != 1 || starts.size(0) != seqs + 1 || starts.scalar_type() != at::kInt || !starts.is_contiguous())
+                refuse(name + ": starts are contiguous int32, one for each sequence and one more");
+        } else if (tokens != seqs) {
+            refuse(name + ": without starts there is one row for each sequence");
+        }
+        if (seqs >= 1 << 20 || tokens >= 1 << 27 || table.size(1) * cache.c.block >= int64_t(1) << 31)
+            refuse(name + ": fewer than 2^20 sequences, 2^27 rows and 2^31 tokens to a row of the table");
+        s = {static_cast<int32_t*>(ptr(table)), static_cast<int32_t*>(ptr(lengths)), static_cast<int32_t*>(ptr(starts)),
+             (uint64_t)(seqs > 1 ? table.stride(0) : table.size(1)), (uint32_t)table.size(1), (uint32_t)seqs, (uint32_t)tokens};
+    }
+};
+
+// [tokens, heads, dim] with adjacent elements along dim.
+struct Heads {
+    uint64_t token, head;   // strides
+    Heads(const at::Tensor& x, const char* what) {
+        if (x.dim() != 3) refuse(std::string(what) + ": [tokens, heads, dim] is needed");
+        if (x.size(2) > 1 && x.stride(2) != 1) refuse(std::string(what) + ": the last dimension must be contiguous");
+        token = x.stride(0);
+        head = x.stride(1);
+    }
+};
+
+// Whether what a call writes meets what it reads.  Rows that lie between others', as columns of one buffer, do not.
+Area area_of(const at::Tensor& t) {
+    if (t.dim() == 3 && t.numel()) {
+        const uint64_t row = (t.size(1) - 1) * t.stride(1) + t.size(2);
+        if ((uint64_t)t.stride(0) >= row) return Area(t, t.size(0), row, t.stride(0));
+    }
+    uint64_t span = t.numel() ? 1 : 0;
+    for (int64_t d = 0; span && d < t.dim(); ++d) span += (t.size(d) - 1) * t.stride(d);
+    return Area(t, span ? 1 : 0, span, span);
+}
+template <typename... Ts>
+bool meets(const at::Tensor& out, const Ts&... inputs) {
+    const Area a = area_of(out);
+    return ((inputs.defined() && a.meets(area_of(inputs))) || ...);
+}
+
+void changed(const at::Tensor& t) {   // for what autograd has kept of it
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// (cache's six, k, v, table, lengths, starts) -> None
+PyObject* cache_write_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
+    return entry(count, 11, [&]() -> PyObject* {
+        const char* name = "cache_write_q8";
+        const Cache cache(args);
+        const at::Tensor &k = tensor(args[6], "cache_write_q8: k"), &v = tensor(args[7], "cache_write_q8: v");
+        const Heads kh(k, "cache_write_q8: k"), vh(v, "cache_write_q8: v");
+        check(is_float(k.scalar_type()), k.scalar_type(), "cache_write_q8: k");
+        if (k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type()) refuse("cache_write_q8: v has k's shape and type");
+        if (k.size(1) != cache.c.heads || k.size(2) != cache.c.dim)
+            refuse("cache_write_q8: k and v have the cache's heads and dim");
+        const Sequences seqs(args + 8, cache, k.size(0), name);
+        recorded(name, k, v, cache.k_scale, cache.v_scale);   // codes and scales are constants to what follows
+        if (at::GradMode::is_enabled() && (cache.k_scale.requires_grad() || cache.v_scale.requires_grad()))
+            refuse("cache_write_q8: scales that gradients are recorded for can not be written");
+        for (const at::Tensor& t : {cache.k, cache.v, cache.k_scale, cache.v_scale})
+            if (meets(t, k, v, seqs.table, seqs.lengths, seqs.starts)) refuse("cache_write_q8: the cache overlaps what is read");
+        const Here here(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts);
+        void* stream = here.stream();
+        int rc;
+        {
+            NoGil free;
+            rc = lecb_cache_write_q8(&cache.c, &seqs.s, ptr(k), ptr(v), type_of(k.scalar_type()), kh.token, kh.head, vh.token,
+                                     vh.head, stream);
+        }
+        done(rc, "lecb_cache_write_q8");
+        for (const at::Tensor& t : {cache.k, cache.v, cache.k_scale, cache.v_scale}) changed(t);
+        return share(Py_None);
+    });
+}
+
+// (cache's six, table, lengths, starts, rows, dtype) -> (k, v)
+PyObject* cache_read_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
+    return entry(count, 11, [&]() -> PyObject* {
+        const char* name = "cache_read_q8";
+        const Cache cache(args);
+        const int64_t tokens = integer(args[9]);
+        if (tokens < 0) refuse("cache_read_q8: the number of rows is not negative");
+        const Sequences seqs(args + 6, cache, tokens, name);
+        const at::ScalarType t = dtype(args[10], name);
+        check(is_float(t), t, name);
+        const bool grads = recorded(name, cache.k_scale, cache.v_scale);
+        const Here here(cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts);
+        const at::Tensor k = make({tokens, cache.c.heads, cache.c.dim}, t, cache.k);
+        const at::Tensor v = make({tokens, cache.c.heads, cache.c.dim}, t, cache.k);
+        void* stream = here.stream();
+        int rc;
+        {
+            NoGil free;
+            rc = lecb_cache_read_q8(&cache.c, &seqs.s, ptr(k), ptr(v), type_of(t), 1, stream);
+        }
+        done(rc, "lecb_cache_read_q8");
+        if (grads) no_backward(name, {k, v}, cache.k_scale, cache.v_scale);
+        return tuple(THPVariable_Wrap(k), THPVariable_Wrap(v));
+    });
+}
+
+// (cache's six, q, table, lengths, starts, scale, causal, window, out, ws) -> out
+PyObject* attention_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
+    return entry(count, 15, [&]() -> PyObject* {
+        const char* name = "attention_q8";
+        const Cache cache(args);
+        const at::Tensor& q = tensor(args[6], name);
+        const Heads qh(q, name);
+        const at::ScalarType t = q.scalar_type();
+        check(is_float(t), t, name);
+        const int64_t tokens = q.size(0), heads = q.size(1);
+        if (q.size(2) != cache.c.dim || heads < 1 || heads % cache.c.heads)
+            refuse("attention_q8: q has the cache's dim and a multiple of its heads");
+        const Sequences seqs(args + 7, cache, tokens, name);
+        double scale = 1.0 / std::sqrt((double)cache.c.dim);
+        if (args[10] != Py_None) {
+            scale = PyFloat_AsDouble(args[10]);
+            if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+        }
+        if (!std::isfinite((float)scale)) refuse("attention_q8: scale is a finite number");
+        const int causal = PyObject_IsTrue(args[11]);
+        if (causal < 0) throw python_error();
+        const int64_t window = args[12] == Py_None ? 0 : integer(args[12]);
+        if (args[12] != Py_None && (window < 1 || window >= int64_t(1) << 31 || !causal))
+            refuse("attention_q8: window is 1 to 2^31 - 1 tokens and goes with causal attention");
+        if (tokens * heads >= 1 << 27 || (int64_t)seqs.s.seqs * cache.c.heads >= 1 << 22)
+            refuse("attention_q8: fewer than 2^27 rows by heads, and 2^22 sequences by the cache's heads");
+        at::Tensor out = optional(args[13], "attention_q8: out"), ws = optional(args[14], "attention_q8: ws");
+        const bool given = out.defined();
+        const bool grads = recorded(name, q, cache.k_scale, cache.v_scale, out);
+        uint64_t ot = heads * cache.c.dim, oh = cache.c.dim;
+        if (given) {
+            if (grads) refuse("attention_q8: out goes with inputs that gradients are not recorded for");
+            if (out.sizes() != q.sizes() || out.scalar_type() != t) refuse("attention_q8: out has q's shape and type");
+            const Heads o(out, "attention_q8: out");
+            ot = tokens > 1 ? o.token : ot;
+            oh = heads > 1 ? o.head : oh;
+            const uint64_t dim = cache.c.dim;
+            if ((tokens > 1 && ot < dim) || (heads > 1 && oh < dim) ||
+                (tokens > 1 && heads > 1 && ot < (heads - 1) * oh + dim && oh < (tokens - 1) * ot + dim))
+                refuse("attention_q8: rows of out overlap");
+            if (meets(out, q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts))
+                refuse("attention_q8: out overlaps what is read");
+            if (tokens == 1 && ot < dim) ot = dim;
+        }
+        if (ws.defined()) {
+            if (ws.scalar_type() != at::kByte || !ws.is_contiguous()) refuse("attention_q8: ws is contiguous uint8");
+            if (meets(ws, q, out, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts))
+                refuse("attention_q8: ws overlaps what is read or written");
+        }
+        const Here here(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts, out, ws);
+        if (!given) out = make(q.sizes(), t, q);
+        if (!ws.defined()) {
+            const int64_t need = (int64_t)lecb_attention_q8_workspace_bytes(&cache.c, seqs.s.seqs, seqs.s.tokens, seqs.s.width,
+                                                                            (uint32_t)heads);
+            if (need) ws = make({need}, at::kByte, q);
+        }
+        void* stream = here.stream();
+        int rc;
+        {
+            NoGil free;
+            rc = lecb_attention_q8(ptr(q), qh.token, qh.head, type_of(t), (uint32_t)heads, &cache.c, &seqs.s, (float)scale, causal,
+                                   (uint32_t)window, ptr(out), ot, oh, !given, ptr(ws), ws.defined() ? ws.nbytes() : 0, stream);
+        }
+        done(rc, "lecb_attention_q8");
+        if (given) changed(out);
+        if (grads) no_backward(name, {out}, q, cache.k_scale, cache.v_scale);
+        return given ? share(args[13]) : THPVariable_Wrap(out);
+    });
+}
+
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef METHODS[] = {METHOD(rmsnorm_q8), METHOD(dequantize_q8), METHOD(matvec_w4), METHOD(quantize_w4),
-                         METHOD(dequantize_w4), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(dequantize_w4), METHOD(cache_write_q8), METHOD(cache_read_q8), METHOD(attention_q8),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef MODULE = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, METHODS, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
