@@ -29,7 +29,8 @@ ARCH = "gfx950"
 SOURCES = ["kernels_misc.hip", "kernels_codebook.hip", "kernels_encode.hip", "kernels_decode.hip", "codebook.cpp",
            "host.cpp", "api.cpp", "noalloc.hip", "kernels_quant.hip", "kernels_matvec.hip", "kernels_matmul.hip",
            "api_layers.cpp",
-           "kernels_cache.hip", "kernels_attend.hip", "api_cache.cpp"]
+           "kernels_cache.hip", "kernels_attend.hip",
+           "api_cache.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -10,7 +10,26 @@
 namespace lecb {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+constexpr int FEW_ROWS = 16, MANY_ROWS = 128;   // of a workgroup, in the two forms
+
+// How one form's work is shared out.  A sequence's rows (tokens x query heads of
+// one head of the cache) go by ROWS at a time, and the tiles that they see are
+// split into parts of one length, chosen from all sequences' lengths so that
+// about `target` workgroups share the whole evenly, whatever the lengths are:
+// one long sequence among short ones is split further.  Numbers of items are
+// bounded on the host by the same sums.  Parts of rows that are split leave their
+// sums in slots of the workspace.
+struct Form {
+    float* ws;
+    uint32_t target;     // workgroups wished for
+    uint32_t shortest;   // tiles that a part has at least
+    uint32_t slots;      // that the workspace holds, for all heads
+};
 
 struct AttendArgs {
     Seqs seqs;
@@ -20,25 +39,15 @@ struct AttendArgs {
     const uint8_t* v;
     const float* k_scale;
     const float* v_scale;
-    float* ws;
     uint64_t q_token, q_head, out_token, out_head;
     uint32_t heads, group, dim;   // of the cache; query heads to each
     uint32_t window;              // 0: none
     int causal, fill;
     float scale;                  // times log2(e)
-    uint32_t target;              // workgroups wished for
-    uint32_t shortest;            // tiles that a part has at least
-    uint32_t items;               // that the grid holds for each head
-    uint32_t slots;               // that the workspace holds
+    uint32_t few;                 // rows of a sequence up to which the form for few takes it
+    Form form[2];                 // few, many
 };
 
-// How the work is shared out.  A sequence's rows (tokens x query heads of one
-// head of the cache) go by `rows` at a time, and the tiles that they see are
-// split into parts of `part` tiles, chosen from all sequences' lengths so that
-// about `target` workgroups share the whole evenly, whatever the lengths are:
-// one long sequence among short ones is split further.  Numbers of items are
-// bounded on the host by the same sums.  Parts of rows that are split leave their
-// sums in slots of the workspace.
 struct Item {
     uint32_t seq, rows_at, part, parts, slot, tiles;   // tiles: of each part
     uint32_t first_tile, last_tile;                    // of the sequence
@@ -49,15 +58,20 @@ struct Load {
 };
 
 template <int ROWS>
+__device__ inline const Form& form_of(const AttendArgs& a) {
+    return a.form[ROWS == MANY_ROWS];
+}
+
+template <int ROWS>
 __device__ inline Load load_of(const AttendArgs& a, uint32_t s) {
     Load l = {0, 0, 0};
     if (s >= a.seqs.seqs) return l;
     const uint32_t n = a.seqs.count(s), len = a.seqs.length(s);
-    if (n == 0) return l;
-    l.rows = (uint32_t)(((uint64_t)n * a.group + ROWS - 1) / ROWS);
+    if (n == 0 || (n * a.group > a.few) != (ROWS == MANY_ROWS)) return l;   // the other form's
+    l.rows = (n * a.group + ROWS - 1) / ROWS;
     if (a.seqs.bad(len) || len == 0) return l;
     const uint32_t at = len > n ? len - n : 0;
-    l.first = a.window && at + 1 > a.window ? (at + 1 - a.window) / TILE_TOKENS : 0;
+    l.first = a.window && at + 1 > a.window ? (at + 1 - a.window) / TILE_TOKENS & ~1u : 0;
     l.tiles = (len + TILE_TOKENS - 1) / TILE_TOKENS - l.first;
     return l;
 }
@@ -79,48 +93,99 @@ __device__ inline uint32_t scan32(uint32_t v, uint32_t lane) {   // of lanes 0 .
     return v;
 }
 
-// Tiles of a part.
+// Tiles of a part, an even number.
 template <int ROWS>
 __device__ inline uint32_t part_tiles(const AttendArgs& a, uint32_t lane) {
+    const Form& f = form_of<ROWS>(a);
     uint64_t all = 0;
     for (uint32_t s0 = 0; s0 < a.seqs.seqs; s0 += 64) {
         const Load l = load_of<ROWS>(a, s0 + lane);
         all += (uint64_t)l.rows * l.tiles;
     }
     all = sum64(all) * a.heads;
-    const uint64_t part = (all + a.target - 1) / a.target;
-    return part > a.shortest ? part < 0x7fffffffu ? (uint32_t)part : 0x7fffffffu : a.shortest;
+    const uint64_t part = (all + f.target - 1) / f.target + 1 & ~1ull;
+    return part > f.shortest ? part < 0x7ffffffeu ? (uint32_t)part : 0x7ffffffeu : f.shortest;
 }
 
 // The item numbered `w`, found by a wave; false: there are only `slot` of them.
-template <int ROWS>
+// With JOIN items are whole rows that were split.
+template <int ROWS, bool JOIN>
 __device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane, Item& it) {
     const uint32_t part = part_tiles<ROWS>(a, lane);
     uint32_t items = 0, slots = 0;   // of the sequences before
     for (uint32_t s0 = 0; s0 < a.seqs.seqs; s0 += 64) {
         const Load l = load_of<ROWS>(a, s0 + lane);
         const uint32_t parts = l.tiles > part ? (l.tiles + part - 1) / part : 1;
-        const uint32_t mine = l.rows * parts, split = parts > 1 ? mine : 0;
+        const uint32_t split = parts > 1 ? l.rows * parts : 0;
+        const uint32_t mine = JOIN ? parts > 1 ? l.rows : 0 : l.rows * parts;
         const uint32_t upto = scan32(mine, lane) + items, slots_upto = scan32(split, lane) + slots;
         const uint64_t hit = __ballot(w < upto);
         if (hit) {
             const int at = __builtin_ctzll(hit);
-            const uint32_t k = w - __shfl(upto - mine, at);
-            it.seq = s0 + at;
-            it.parts = __shfl(parts, at);
-            it.rows_at = k / it.parts;
-            it.part = k % it.parts;
-            it.slot = __shfl(slots_upto - split, at) + k;
-            it.tiles = part;
-            it.first_tile = __shfl(l.first, at);
-            it.last_tile = it.first_tile + __shfl(l.tiles, at);
+            const uint32_t k = w - __shfl(upto - mine, at), each = JOIN ? 1 : __shfl(parts, at);
+            it.seq = uniform(s0 + at);
+            it.parts = uniform(__shfl(parts, at));
+            it.rows_at = uniform(__shfl(l.rows, at) - 1 - k / each);   // the rows that see most come first
+            it.part = uniform(k % each);
+            it.slot = uniform(__shfl(slots_upto - split, at)) + it.rows_at * it.parts + it.part;
+            it.tiles = uniform(part);
+            it.first_tile = uniform(__shfl(l.first, at));
+            it.last_tile = it.first_tile + uniform(__shfl(l.tiles, at));
             return true;
         }
-        items = __shfl(upto, 63);
-        slots = __shfl(slots_upto, 63);
+        items = uniform(__shfl(upto, 63));
+        slots = uniform(__shfl(slots_upto, 63));
     }
     it.slot = items;
     return false;
+}
+
+// What a workgroup of either form works on: rows, and the tiles that they see.
+struct Work {
+    uint32_t begin, rows, r0, have, slot, parts;   // the sequence's first row and their number; of this item
+    int old, len;                                  // tokens before the sequence's rows, and with them
+    int from, to;                                  // tiles
+    int hi_least, lo_most;                         // whole ones are seen by every row
+    bool bad;
+};
+
+template <int ROWS>
+__device__ inline bool work_of(const AttendArgs& a, const Item& it, uint32_t h, Work& k) {
+    const uint32_t n = uniform(a.seqs.count(it.seq)), len = uniform(a.seqs.length(it.seq));
+    k.begin = uniform(a.seqs.begin(it.seq));
+    k.rows = n * a.group;
+    k.slot = it.slot * a.heads + h;
+    k.parts = it.parts;
+    // starts that do not rise make more of either than there is room for
+    if (it.rows_at >= (k.rows + ROWS - 1) / ROWS || (it.parts > 1 && k.slot >= form_of<ROWS>(a).slots)) return false;
+    k.r0 = it.rows_at * ROWS;
+    k.have = k.rows - k.r0 < (uint32_t)ROWS ? k.rows - k.r0 : ROWS;
+    k.bad = a.seqs.bad(len);
+    k.len = (int)len;
+    k.old = (int)len - (int)n;
+    const int first = (int)(k.r0 / a.group), last = (int)((k.r0 + k.have - 1) / a.group), w = (int)a.window;
+    const int hi_most = a.causal ? k.old + last : k.len - 1, lo_least = w ? k.old + first - w + 1 : 0;
+    k.hi_least = a.causal ? k.old + first : k.len - 1;
+    k.lo_most = w ? k.old + last - w + 1 : 0;
+    const uint64_t at = (uint64_t)it.first_tile + (uint64_t)it.part * it.tiles;
+    k.from = (int)at;
+    k.to = (int)it.last_tile;
+    if (at + it.tiles < (uint64_t)k.to) k.to = (int)(at + it.tiles);
+    if (lo_least > 0 && lo_least / (int)TILE_TOKENS > k.from) k.from = lo_least / (int)TILE_TOKENS & ~1;
+    const int seen = hi_most < 0 ? 0 : hi_most / (int)TILE_TOKENS + 1;
+    if (seen < k.to) k.to = seen;
+    return true;
+}
+
+// The rows of a sequence that does not fit its row of the table.
+template <typename T>
+__device__ inline void bad_rows(const AttendArgs& a, const Work& k, uint32_t h) {
+    for (uint32_t i = 0; i < k.have; ++i) {
+        const uint32_t row = k.r0 + i;
+        T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + row / a.group) * a.out_token +
+               (uint64_t)(h * a.group + row % a.group) * a.out_head;
+        for (uint32_t d = threadIdx.x; d < a.dim; d += blockDim.x) o[d] = (T)__uint_as_float(0x7fc00000u);
+    }
 }
 
 // Rows of no sequence, by the workgroups that have no item.
@@ -182,20 +247,77 @@ struct Parts<float> {
 // p = 2^(x + ref), x the score times log2(e), and ref = 30 - max(x + e) where
 // 2^e is the power of two just above the scale of x's values (e >= -60).  So p
 // times that scale, what the second product takes, is at most 2^30 whatever the
-// scales are (2^15 as a half, OUT undoes the rest), with 40 bits below it before
-// halves run out, and p itself stays within 2^90 and 2^-98.
-constexpr float REF_TOP = 30.0f;
-constexpr float P_DOWN = 0x1p-15f;   // into halves
-constexpr float OUT = 0x1p15f;       // and back
+// scales are, with 36 bits below it before halves run out, and p itself stays
+// within 2^90 and 2^-94.  ref follows a larger maximum only once it is LAG behind,
+// as sums have to be scaled whenever it moves: in a prompt of 4096 tokens after
+// nearly each pair of tiles without that, once or twice with it.
+constexpr float REF_TOP = 30.0f, LAG = 4.0f;
+constexpr float P_DOWN = 0x1p-19f;   // into halves: at most 2^(30 + LAG - 19)
+constexpr float OUT = 0x1p19f;       // and back
 constexpr int SCALE_LOW = -60;
 
 __device__ inline float scale_exponent(float s) {
-    // 0, infinities and NaN give 0 or what they stand for below; all that counts is that p stays finite
+    // infinities and NaN give 0, and zero the lowest: all that counts is that p stays finite
     const int e = __builtin_amdgcn_frexp_expf(s);
     return (float)(s == 0.0f ? SCALE_LOW : e > SCALE_LOW ? e : SCALE_LOW);
 }
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ inline uint32_t of_lane(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ inline float of_lane(float v, int lane) { return __uint_as_float(of_lane(__float_as_uint(v), lane)); }
+// The largest of the lanes 32 apart, and of those 16 apart.
+__device__ inline float max_of_halves(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ inline float max_of_quarters(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return max_of_halves(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+}
 __device__ inline float inf() { return __uint_as_float(0x7f800000u); }
+
+// One row of q as operands: N pieces of eight dimensions, d0 + step i and on; the
+// lanes that share a row are LANES apart.  Returns what takes a product of codes to a score.
+template <typename T, int N, int LANES>
+__device__ inline float load_row(const AttendArgs& a, const Work& k, uint32_t row, uint32_t h, uint32_t d0, uint32_t step,
+                                 f16x8 (&q)[N][Parts<T>::Q]) {
+    const bool real = row < k.rows;
+    const uint32_t token = real ? row / a.group : 0, head = real ? row % a.group : 0;
+    const T* p = reinterpret_cast<const T*>(a.q) + (real ? (uint64_t)(k.begin + token) * a.q_token : 0) +
+                 (uint64_t)(h * a.group + head) * a.q_head;
+    Piece<T> x[N];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const uint32_t d = step * u + d0, count = real && d < a.dim ? a.dim - d : 0;
+        x[u].load(p + (count ? d : 0), count);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(x[u][e]) & 0x7fffffffu;
+            top = b > top ? b : top;
+        }
+#pragma unroll
+    for (int o = LANES; o < 64; o <<= 1) {
+        const uint32_t b = __shfl_xor(top, o);
+        top = b > top ? b : top;
+    }
+    int lift = 0;
+    if (Parts<T>::LIFT && top != 0) lift = 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top));
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float f = Parts<T>::LIFT ? ldexpf(x[u][e], lift) : x[u][e];
+#pragma unroll
+            for (int j = 0; j < Parts<T>::Q; ++j) {
+                q[u][j][e] = (_Float16)f;
+                f -= (float)q[u][j][e];
+            }
+        }
+    return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : ldexpf(a.scale, -lift);
+}
 
 }  // namespace lecb
 #endif

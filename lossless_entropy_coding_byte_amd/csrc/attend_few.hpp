@@ -1,0 +1,244 @@
+// Attention over the 8-bit cache: the form for few rows (decoding steps).
+#pragma once
+
+#include "attend.hpp"
+
+#if defined(__HIPCC__)
+namespace lecb {
+
+// A tile of 32 tokens, in registers as it lies.
+template <int U>
+struct Tile {
+    u32x4 k[U], v[U];
+    float scales;   // of keys in even lanes, of values in odd ones
+    bool none;      // the table names no block of the cache
+    __device__ void load(const AttendArgs& a, uint32_t page, uint32_t t, uint32_t shift, uint32_t h, uint32_t lane) {
+        none = page >= a.seqs.blocks;
+        const uint64_t cell = (uint64_t)(none ? 0 : page) * a.heads + h;
+        const uint64_t at = ((cell << shift) + (t & ((1u << shift) - 1))) * (U * UNIT_BYTES) + lane * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            k[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.k + at + u * UNIT_BYTES));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.v + at + u * UNIT_BYTES));
+        scales = (lane & 1 ? a.v_scale : a.k_scale)[cell];
+    }
+    __device__ float k_scale() const { return none ? __uint_as_float(0x7fc00000u) : of_lane(scales, 0); }
+    __device__ float v_scale() const { return of_lane(scales, 1); }
+};
+
+// Few rows: a workgroup takes 16 NT rows of one head over a part of the tiles,
+// its waves tile by tile in turn, each with a softmax of its own; their sums are
+// joined at the end.  Matrix instructions by 16 x 16 x 32, transposed: codes of
+// 16 tokens (then of 16 dimensions of the values) times the rows, so that a row's
+// scores stand in one lane of each 16, four tokens each, and are the second
+// product's operand as they are; values are stored in that order of tokens.
+// Neither codes nor scores go through LDS.
+template <int NT, int WAVES>
+struct FewMemory {
+    float sum[WAVES][16 * NT][68];
+    float ref[WAVES][16 * NT], l[WAVES][16 * NT];
+};
+
+template <typename T, int U, int NT, int WAVES>
+__device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<NT, WAVES>& mem) {
+    constexpr int ROWS = 16 * NT, NQ = Parts<T>::Q, NP = Parts<T>::P, THREADS = 64 * WAVES;
+    const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    Work k;
+    if (!work_of<ROWS>(a, it, h, k)) return;
+    if (k.bad) {
+        bad_rows<T>(a, k, h);
+        return;
+    }
+    const uint32_t seq = it.seq;
+
+    // rows: lane r of each 16 has row r of each 16, dimensions 32 u + 8 g and on
+    f16x8 q[NT][U][NQ];
+    float factor[NT];
+    int hi[NT], lo[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        const uint32_t row = k.r0 + 16 * c + r;
+        factor[c] = load_row<T, U, 16>(a, k, row, h, 8 * g, 32, q[c]);
+        const int at = k.old + (row < k.rows ? (int)(row / a.group) : 0);
+        hi[c] = a.causal ? at : k.len - 1;
+        lo[c] = a.window ? at - (int)a.window + 1 : 0;
+    }
+    const int from = k.from, to = k.to, lo_most = k.lo_most, hi_least = k.hi_least;
+
+    f32x4 acc[NT][2 * U];
+    float ref[NT], sum[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        ref[c] = inf();
+        sum[c] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * U; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const uint32_t shift = __builtin_ctz(a.seqs.block / TILE_TOKENS);
+
+    auto compute = [&](int t, const Tile<U>& x) {
+        f32x4 s[NT][2];
+#pragma unroll
+        for (int c = 0; c < NT; ++c) s[c][0] = s[c][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const f16x8 codes = operand(x.k[u][2 * b], x.k[u][2 * b + 1]);
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j)
+                        s[c][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, q[c][u][j], s[c][b], 0, 0, 0);
+            }
+        const float ks = x.k_scale(), vs = x.v_scale(), unit = scale_exponent(vs);
+        const int at = t * (int)TILE_TOKENS;
+        // all rows see all of the tile's tokens, and the larger product is the larger score
+        const bool plain = at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f;
+        const bool number = fabsf(vs) < inf();
+        const float down = number ? vs * P_DOWN : 0.0f;
+        f16x8 p[NT][NP];
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            float f = factor[c] * ks, v[8], most = -inf();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = s[c][i / 4][i % 4];
+            if (!plain) {
+                asm volatile("");   // not to be done and then selected from
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int pos = at + 4 * (int)g + i % 4 + i / 4 * 16;
+                    v[i] = pos <= hi[c] && pos >= lo[c] ? v[i] * f : -inf();
+                }
+                f = 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, v[i]);
+            most = max_of_quarters(most * f);
+            // values without a number to scale them: no number to the rows that see one of them
+            if (!number && most != -inf()) sum[c] = __uint_as_float(0x7fc00000u);
+            const float next = REF_TOP - (most + unit);
+            if (__ballot(next < ref[c] - LAG)) {
+                const float down_by = next < ref[c] ? exp2_of(next - ref[c]) : 1.0f;
+                sum[c] *= down_by;
+#pragma unroll
+                for (int i = 0; i < 2 * U; ++i) acc[c][i] *= down_by;
+                ref[c] = fminf(ref[c], next);
+            }
+            const float base = ref[c] == inf() ? 0.0f : ref[c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = exp2_of(fmaf(v[i], f, base));
+                sum[c] += v[i];
+                v[i] *= down;
+            }
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[c][j][i] = (_Float16)v[i];
+                    v[i] -= (float)p[c][j][i];
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const f16x8 codes = operand(x.v[u][2 * b], x.v[u][2 * b + 1]);
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        acc[c][2 * u + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, p[c][j], acc[c][2 * u + b], 0, 0, 0);
+            }
+    };
+    int t = from + (int)wave;
+    if (t < to) {
+        // the next tile's loads are in flight while one is worked on, its block's number one more ahead;
+        // past the last tile the same one is asked for again
+        Tile<U> x, y;
+        auto page = [&](int i) { return uniform(a.seqs.page(seq, (uint32_t)(i < to ? i : t) >> shift)); };
+        x.load(a, page(t), t, shift, h, lane);
+        uint32_t ahead = page(t + WAVES);
+        while (true) {
+            int next = t + WAVES < to ? t + WAVES : t;
+            y.load(a, ahead, next, shift, h, lane);
+            ahead = page(t + 2 * WAVES);
+            compute(t, x);
+            t += WAVES;
+            if (t >= to) break;
+            next = t + WAVES < to ? t + WAVES : t;
+            x.load(a, ahead, next, shift, h, lane);
+            ahead = page(t + 2 * WAVES);
+            compute(t, y);
+            t += WAVES;
+            if (t >= to) break;
+        }
+    }
+
+    // the waves' sums, joined in their order
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        sum[c] += __shfl_xor(sum[c], 16);
+        sum[c] += __shfl_xor(sum[c], 32);
+        if (g == 0) {
+            mem.ref[wave][16 * c + r] = ref[c];
+            mem.l[wave][16 * c + r] = sum[c];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        float least = mem.ref[0][16 * c + r];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) least = fminf(least, mem.ref[i][16 * c + r]);
+        const float down_by = ref[c] == least ? 1.0f : exp2_of(least - ref[c]);
+#pragma unroll
+        for (int i = 0; i < 2 * U; ++i) acc[c][i] *= down_by;
+    }
+    float* ws = form_of<ROWS>(a).ws + (uint64_t)k.slot * ROWS * (32 * U + 4);
+#pragma unroll
+    for (int d0 = 0; d0 < U; d0 += 2) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (2 * d0 + i < 2 * U)
+                    *reinterpret_cast<f32x4*>(&mem.sum[wave][16 * c + r][16 * i + 4 * g]) = acc[c][2 * d0 + i];
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < ROWS * 16; i += THREADS) {
+            const uint32_t row = i / 16, d = i % 16 * 4;
+            if (row >= k.have) break;
+            f32x4 v = *reinterpret_cast<const f32x4*>(&mem.sum[0][row][d]);
+#pragma unroll
+            for (int j = 1; j < WAVES; ++j) v += *reinterpret_cast<const f32x4*>(&mem.sum[j][row][d]);
+            float least = mem.ref[0][row], l = 0.0f;
+#pragma unroll
+            for (int j = 1; j < WAVES; ++j) least = fminf(least, mem.ref[j][row]);
+#pragma unroll
+            for (int j = 0; j < WAVES; ++j) l += mem.l[j][row] * (mem.ref[j][row] == least ? 1.0f : exp2_of(least - mem.ref[j][row]));
+            const uint32_t at = 32 * d0 + d;
+            if (k.parts > 1) {
+                if (at < 32 * U) *reinterpret_cast<f32x4*>(ws + row * (32 * U + 4) + 4 + at) = v;
+                if (at == 0) {
+                    ws[row * (32 * U + 4)] = least;
+                    ws[row * (32 * U + 4) + 1] = l;
+                }
+            } else {
+                const float up = l == 0.0f ? 0.0f : OUT / l;
+                const uint32_t i = k.r0 + row;
+                T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + i / a.group) * a.out_token +
+                       (uint64_t)(h * a.group + i % a.group) * a.out_head + at;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (at + j < a.dim) o[j] = (T)(v[j] * up);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace lecb
+#endif

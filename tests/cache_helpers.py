@@ -82,7 +82,8 @@ def attention(q, cache, table, lengths, starts=None, scale=None, causal=True, wi
       by twice its most;
     * a weight's rounding for the second product: 2^-11 where results are bfloat16, else 2^-22;
     * sums: parts of 32, one after another: (48 + n / 32) 2^-24 of A, twice with the denominator;
-    * halves run out 2^-40 below the largest weight times its scale: half of that, times codes to 127, for each token;
+    * halves, whose smallest step is 2^-24, hold the largest weight times its scale as 2^11 or more: half a step, 2^-36 of it,
+      times codes to 127, for each token;
     * the last rounding, half a step."""
     k, v = values(cache)
     q64, dim, block = q.cpu().double(), cache.dim, cache.block
@@ -113,7 +114,7 @@ def attention(q, cache, table, lengths, starts=None, scale=None, causal=True, wi
             out[row] = (p @ vv).reshape(-1, dim)
             a = (p @ vv.abs())
             e = 2 * ((dim + 8) * 2.0**-24 * size + 2.0**-22) + weight + 2 * (48 + (hi - lo) / 32) * 2.0**-24
-            low = 127 * (hi - lo) * 2.0**-40 * (p * steps[:, None, lo:hi]).amax(2, keepdim=True)
+            low = 127 * (hi - lo) * 2.0**-36 * (p * steps[:, None, lo:hi]).amax(2, keepdim=True)
             tol[row] = (2 * e * a + low).reshape(-1, dim)
     return out, tol + HALF_STEP[q.dtype] * (out.abs() + tol) + SMALLEST[q.dtype]
 
