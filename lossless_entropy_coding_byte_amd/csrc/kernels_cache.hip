@@ -31,22 +31,32 @@ struct Span {
     uint32_t lo, hi;             // tokens lo .. hi - 1 of the block are rows; none: lo == hi
     uint32_t row;                // of token lo
     bool bad;
-    __device__ bool find(const Seqs& q, uint32_t w) {
-        uint32_t s = 0, skip = 0;
+    // Called by whole waves: 64 sequences are looked at in one load, so that 4096 take two.
+    __device__ bool find(const Seqs& q, uint32_t w, uint32_t lane) {
+        uint32_t s = 0, skip = 0, begin, n, len;
         if (q.starts) {
-            uint32_t end = q.seqs;   // the last sequence whose numbers begin at w or before
-            while (end - s > 1) {
-                const uint32_t mid = (s + end) / 2;
-                if (q.begin(mid) / q.block + 2 * mid <= w)
-                    s = mid;
-                else
-                    end = mid;
+            uint32_t step = 1;
+            while ((uint64_t)step * 64 < q.seqs) step *= 64;
+            for (;; step /= 64) {   // the last sequence whose numbers begin at w or before
+                const uint32_t mine = umin(s + lane * step, q.seqs - 1);
+                begin = q.begin(mine);
+                n = q.count(mine);   // what the last round needs of the one that it finds
+                len = q.length(mine);
+                const uint64_t after = __ballot(lane > 0 && (s + lane * step >= q.seqs || begin / q.block + 2 * mine > w));
+                const int at = (after ? __builtin_ctzll(after) : 64) - 1;
+                s = __builtin_amdgcn_readfirstlane(s + at * step);
+                if (step > 1) continue;
+                begin = __builtin_amdgcn_readlane(begin, at);
+                n = __builtin_amdgcn_readlane(n, at);
+                len = __builtin_amdgcn_readlane(len, at);
+                break;
             }
-            skip = w - (q.begin(s) / q.block + 2 * s);   // starts that do not rise wrap around: past every block
+            skip = w - (begin / q.block + 2 * s);   // starts that do not rise wrap around: past every block
         } else {
-            s = w;
+            s = begin = w;
+            n = 1;
+            len = q.length(s);
         }
-        const uint32_t n = q.count(s), len = q.length(s);
         seq = s;
         bad = q.bad(len);
         const uint32_t first = len > n ? len - n : 0;   // tokens first .. len - 1
@@ -56,7 +66,7 @@ struct Span {
         const uint32_t at = index * q.block;
         lo = first > at ? first - at : 0;
         hi = umin(len - at, q.block);
-        row = q.begin(s) + (at + lo - len + n);   // n > len: the first rows have no token
+        row = begin + (at + lo - len + n);   // n > len: the first rows have no token
         page = bad ? 0xffffffffu : q.page(s, index);
         bad = bad || page >= q.blocks;
         return true;
@@ -76,22 +86,57 @@ __device__ inline uint32_t value_byte(uint32_t t, uint32_t d) {
 // neighbour, e = x - n s is exact in one fused operation, and comparing |e| with
 // s / 2 settles it.  Scales below 2^-60 go times 2^64, so that 1 / s stays in range.
 struct Step {
-    float s, inv, t, lift;
-    __device__ void set(float scale) {
-        s = scale;
+    float inv, t, lift;   // 1 / t, 0 where there is none; t = s lift
+    __device__ void set(float s) {
         lift = s < 0x1p-60f ? 0x1p64f : 1.0f;
         t = s * lift;
         inv = s > 0.0f && s < __uint_as_float(INF_BITS) ? 1.0f / t : 0.0f;
     }
-    __device__ int code(float x) const {
-        const float v = x * lift;
-        float n = rintf(v * inv);
-        const float e = fmaf(-n, t, v), a = fabsf(e) + fabsf(e);
-        if (a > t || (a == t && ((int)n & 1))) n += e > 0.0f ? 1.0f : -1.0f;
-        n = fminf(fmaxf(n, -127.0f), 127.0f);
-        return inv > 0.0f ? (int)n : 0;
-    }
 };
+
+// Eight codes, in the order of their bytes.  Adding MAGIC to x inv, in one fused
+// operation, rounds it to n and leaves n in the lowest byte.  Where the largest |e|
+// of the eight does not settle them (16-bit numbers are half of the block's
+// largest, half a step between two codes, often enough), n moves towards e if
+// |e| > s / 2, or |e| = s / 2 and n is odd.
+__device__ inline u32x2 codes_of(const Step& k, const float (&x)[8]) {
+    constexpr float MAGIC = 12582912.0f;   // 1.5 2^23
+    if (!(k.inv > 0.0f)) return u32x2{0, 0};
+    float worst = 0.0f;
+    uint32_t m[8];
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = x[i] * k.lift, f = fmaf(v, k.inv, MAGIC);
+        m[i] = __float_as_uint(f);
+        e[i] = fmaf(MAGIC - f, k.t, v);
+        worst = fmaxf(worst, fabsf(e[i]));
+    }
+    const float half = 0.5f * k.t;
+    if (worst >= half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint(e[i]);
+            const bool off = (b & ABS_MASK) + (m[i] & 1) > __float_as_uint(half);
+            m[i] += off ? (uint32_t)((int)b >> 31 | 1) : 0;
+        }
+    }
+    if (k.lift != 1.0f) {   // a scale rounded down at the bottom of the range leaves more than 127 steps
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = (int)(m[i] - __float_as_uint(MAGIC));
+            m[i] = (uint32_t)(n > 127 ? 127 : n < -127 ? -127 : n);
+        }
+    }
+    u32x2 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x0c0c0400u);
+        w[i] = lo | hi << 16;
+    }
+    return w;
+}
 
 struct WriteArgs {
     Seqs seqs;
@@ -102,33 +147,65 @@ struct WriteArgs {
     uint32_t heads, dim, units;
 };
 
+// Work within a block goes by tokens of a chunk (64 of 128 dimensions, 8 KiB of codes), in pieces of
+// four tokens x eight dimensions, one a thread.
+__device__ inline uint32_t chunk_tokens(uint32_t units) { return units <= 2 ? 128 : units <= 4 ? 64 : 32; }
+
+// A chunk's codes in LDS: the 256 bytes of a unit that 16 lanes load lie 272 apart,
+// so that pieces of neighbouring dimensions and tokens meet other banks.
+constexpr uint32_t PITCH = 272;
+__device__ inline uint32_t padded_at(uint32_t byte) { return byte / 256 * PITCH + byte % 256; }
+
+struct Piece4 {
+    uint32_t t, d;   // first token (of the chunk) and dimension
+    bool real;
+    __device__ Piece4(uint32_t i, uint32_t tokens, uint32_t dim) {
+        const uint32_t across = (dim + 7) / 8;
+        t = i / across * 4;
+        d = i % across * 8;
+        real = t < tokens;
+    }
+};
+
 // A workgroup writes the rows of one span for one head, keys or values: their
-// largest magnitude first, then the codes by tiles of 32 tokens, put together in
-// LDS in the order of a tile and stored by 16-byte pieces.
+// largest magnitude first, then the codes.  A block of one chunk stays in
+// registers in between.  Codes of chunks that hold new tokens alone (or nothing
+// yet behind them) are put together in LDS and stored by 16-byte pieces; where
+// older tokens share the chunk, as in a decoding step, each goes to its own place.
 template <typename T>
-__global__ __launch_bounds__(THREADS) void cache_write_kernel(WriteArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t s_tile[8 * UNIT_BYTES];
+__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 6 : 4) void cache_write_kernel(WriteArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t s_codes[32 * PITCH];
     __shared__ uint32_t s_max[THREADS / 64];
     Span p;
-    if (!p.find(a.seqs, blockIdx.x) || p.bad) return;
-    const uint32_t which = blockIdx.z, h = blockIdx.y, block = a.seqs.block;
-    const uint64_t cell = (uint64_t)p.page * a.heads + h;
+    if (!p.find(a.seqs, blockIdx.x, threadIdx.x & 63) || p.bad) return;
+    const uint32_t which = blockIdx.z, h = blockIdx.y, block = a.seqs.block, dim = a.dim;
+    const uint64_t cell = (uint64_t)p.page * a.heads + h, stride = a.token[which];
     const T* x = reinterpret_cast<const T*>(a.x[which]) + h * a.head[which];
-    const uint64_t stride = a.token[which];
-    const uint32_t pieces = (a.dim + 7) / 8, count = (p.hi - p.lo) * pieces;
+    const float was = a.scale[which][cell];
+    const uint32_t chunk = umin(chunk_tokens(a.units), block), first = p.lo / chunk * chunk;
 
-    uint32_t amax = 0;
-    for (uint32_t i = threadIdx.x; i < count; i += THREADS) {
-        const uint32_t t = i / pieces, d = i % pieces * 8;
-        Piece<T> v;
-        v.load(x + (uint64_t)(p.row + t) * stride + d, a.dim - d);
+    // a piece's tokens, zeros where they are not new
+    auto load = [&](uint32_t begin, const Piece4& c, Piece<T> (&v)[4]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = umax(amax, __float_as_uint(v[e]) & ABS_MASK);
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t t = begin + c.t + j;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j].set(i, 0.0f);
+            if (c.real && t >= p.lo && t < p.hi) v[j].load(x + (uint64_t)(p.row + t - p.lo) * stride + c.d, dim - c.d);
+        }
+    };
+    Piece<T> v[4];
+    uint32_t amax = 0;
+    for (uint32_t begin = first; begin < p.hi; begin += chunk) {
+        load(begin, Piece4(threadIdx.x, chunk, dim), v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = umax(amax, __float_as_uint(v[j][e]) & ABS_MASK);
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) amax = umax(amax, (uint32_t)__shfl_xor((int)amax, o));
     if ((threadIdx.x & 63) == 0) s_max[threadIdx.x / 64] = amax;
-    const float was = a.scale[which][cell];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < THREADS / 64; ++i) amax = umax(amax, s_max[i]);
@@ -138,59 +215,95 @@ __global__ __launch_bounds__(THREADS) void cache_write_kernel(WriteArgs a) {
     if (kept && need <= was) scale = was;
     if (kept && need > was) scale = fmaxf(need, 1.25f * was);
     if (kept && !(was == was)) scale = was;
-    const bool grow = kept && __float_as_uint(scale) != __float_as_uint(was);
     if (threadIdx.x == 0) a.scale[which][cell] = scale;
     Step step;
     step.set(scale);
 
     const uint32_t tile_bytes = a.units * UNIT_BYTES;
     uint8_t* out = a.codes[which] + cell * (block / TILE_TOKENS) * tile_bytes;
-    for (uint32_t tile = grow ? 0 : p.lo / TILE_TOKENS; tile * TILE_TOKENS < p.hi; ++tile) {
-        const uint32_t begin = tile * TILE_TOKENS;
-        u32x4* mem = reinterpret_cast<u32x4*>(out + (uint64_t)tile * tile_bytes);
-        for (uint32_t i = threadIdx.x; i < tile_bytes / 16; i += THREADS) {
-            u32x4 w = {0, 0, 0, 0};
-            if (begin < p.lo) w = mem[i];
-            if (grow) {
-                // codes of 8 bits by scales of 24: exact quotients in 64 bits never lie so near to half a step that rounding could cross it
+    if (kept && __float_as_uint(scale) != __float_as_uint(was)) {
+        // the older codes' tiles, rounded again: codes of 8 bits by scales of 24 give quotients that never lie
+        // nearer to half a step than 64 bits tell
+        u32x4* mem = reinterpret_cast<u32x4*>(out);
+        const uint32_t n = (p.lo + TILE_TOKENS - 1) / TILE_TOKENS * tile_bytes / 16;
+        for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
+            u32x4 w = mem[i];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t r = 0;
+            for (int j = 0; j < 4; ++j) {
+                uint32_t r = 0;
 #pragma unroll
-                    for (int b = 0; b < 32; b += 8) {
-                        const double v = (double)(int8_t)(w[j] >> b) * (double)was / (double)scale;
-                        const int q = step.inv > 0.0f ? (int)fmin(fmax(rint(v), -127.0), 127.0) : 0;
-                        r |= (uint32_t)(q & 255) << b;
-                    }
-                    w[j] = r;
+                for (int b = 0; b < 32; b += 8) {
+                    const double q = (double)(int8_t)(w[j] >> b) * (double)was / (double)scale;
+                    const int n = step.inv > 0.0f ? (int)fmin(fmax(rint(q), -127.0), 127.0) : 0;
+                    r |= (uint32_t)(n & 255) << b;
                 }
+                w[j] = r;
             }
-            reinterpret_cast<u32x4*>(s_tile)[i] = w;
+            mem[i] = w;
         }
-        __syncthreads();
-        const uint32_t from = begin > p.lo ? begin : p.lo, to = umin(begin + TILE_TOKENS, p.hi);
-        if (from < to) {
-            const uint32_t n = (to - from) * pieces;
-            for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
-                const uint32_t t = from + i / pieces, d = i % pieces * 8;
-                Piece<T> v;
-                v.load(x + (uint64_t)(p.row + t - p.lo) * stride + d, a.dim - d);
-                uint32_t q[8];
+        __syncthreads();   // new codes go over these
+    }
+
+    for (uint32_t begin = first; begin < p.hi; begin += chunk) {
+        const Piece4 c(threadIdx.x, chunk, dim);
+        if (block > chunk) load(begin, c, v);
+        u32x2 q[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q[e] = (uint32_t)step.code(v[e]) & 255u;
-                uint8_t* unit = s_tile + d / 32 * UNIT_BYTES;
+        for (int j = 0; j < 4; ++j) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = v[j][e];
+            q[j] = codes_of(step, f);
+        }
+        uint8_t* mem = out + begin / TILE_TOKENS * tile_bytes;
+        const uint32_t unit = (c.t / TILE_TOKENS * a.units + c.d / 32) * UNIT_BYTES, t = c.t % TILE_TOKENS, d = c.d % 32;
+        if (begin < p.lo) {
+            if (!c.real) continue;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                if (begin + c.t + j < p.lo || begin + c.t + j >= p.hi) continue;
                 if (which == 0) {
-                    u32x2 w = {q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24};
-                    *reinterpret_cast<u32x2*>(unit + key_byte(t % TILE_TOKENS, d % 32)) = w;
+                    *reinterpret_cast<u32x2*>(mem + unit + key_byte(t + j, d)) = q[j];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) unit[value_byte(t % TILE_TOKENS, d % 32 + e)] = (uint8_t)q[e];
+                    for (uint32_t e = 0; e < 8; ++e)
+                        mem[unit + value_byte(t + j, d + e)] = (uint8_t)(q[j][e / 4] >> (8 * (e % 4)));
+                }
+            }
+            continue;
+        }
+        // dimensions past the head's and tokens past the last are zeros
+        const uint32_t bytes = chunk / TILE_TOKENS * tile_bytes;
+        if (dim <= (a.units - 1) * 32 + 24) {
+            for (uint32_t i = threadIdx.x; i < bytes / 16; i += THREADS)
+                *reinterpret_cast<u32x4*>(s_codes + padded_at(i * 16)) = u32x4{0, 0, 0, 0};
+            __syncthreads();
+        }
+        if (c.real) {
+            if (which == 0) {
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+                    *reinterpret_cast<u32x2*>(s_codes + padded_at(unit + key_byte(t + j, d))) = q[j];
+            } else {
+                // four tokens' codes of a dimension are a word
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t a0 = __builtin_amdgcn_perm(q[1][i], q[0][i], 0x05010400u);   // 0 and 1 of tokens 0, 1
+                    const uint32_t a1 = __builtin_amdgcn_perm(q[1][i], q[0][i], 0x07030602u);   // 2 and 3
+                    const uint32_t b0 = __builtin_amdgcn_perm(q[3][i], q[2][i], 0x05010400u);
+                    const uint32_t b1 = __builtin_amdgcn_perm(q[3][i], q[2][i], 0x07030602u);
+                    const uint32_t r[4] = {__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                                           __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint32_t*>(s_codes + padded_at(unit + value_byte(t, d + 4 * i + e))) = r[e];
                 }
             }
         }
         __syncthreads();
-        for (uint32_t i = threadIdx.x; i < tile_bytes / 16; i += THREADS) mem[i] = reinterpret_cast<u32x4*>(s_tile)[i];
-        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < bytes / 16; i += THREADS)
+            reinterpret_cast<u32x4*>(mem)[i] = *reinterpret_cast<const u32x4*>(s_codes + padded_at(i * 16));
+        if (block > chunk) __syncthreads();
     }
 }
 
@@ -211,7 +324,7 @@ __device__ void put_row(T* out, uint32_t dim, float v) {
 
 template <typename T>
 __global__ __launch_bounds__(THREADS) void cache_read_kernel(ReadArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t s_tile[8 * UNIT_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t s_codes[32 * PITCH];
     const uint32_t which = blockIdx.z, h = blockIdx.y, block = a.seqs.block;
     T* out = reinterpret_cast<T*>(a.out[which]) + (uint64_t)h * a.dim;
     const uint64_t stride = (uint64_t)a.heads * a.dim;
@@ -228,33 +341,54 @@ __global__ __launch_bounds__(THREADS) void cache_read_kernel(ReadArgs a) {
         return;
     }
     Span p;
-    if (!p.find(a.seqs, blockIdx.x)) return;
+    if (!p.find(a.seqs, blockIdx.x, threadIdx.x & 63)) return;
     if (p.bad) {
         for (uint32_t i = 0; i < p.hi - p.lo; ++i)
             put_row(out + (uint64_t)(p.row + i) * stride, a.dim, __uint_as_float(0x7fc00000u));
         return;
     }
     const uint64_t cell = (uint64_t)p.page * a.heads + h;
-    const uint32_t pieces = (a.dim + 7) / 8, tile_bytes = a.units * UNIT_BYTES;
+    const uint32_t tile_bytes = a.units * UNIT_BYTES, chunk = umin(chunk_tokens(a.units), block);
     const uint8_t* in = a.codes[which] + cell * (block / TILE_TOKENS) * tile_bytes;
     const float scale = a.scale[which][cell];
-    for (uint32_t tile = p.lo / TILE_TOKENS; tile * TILE_TOKENS < p.hi; ++tile) {
-        const uint32_t begin = tile * TILE_TOKENS;
-        const u32x4* mem = reinterpret_cast<const u32x4*>(in + (uint64_t)tile * tile_bytes);
-        for (uint32_t i = threadIdx.x; i < tile_bytes / 16; i += THREADS) reinterpret_cast<u32x4*>(s_tile)[i] = mem[i];
+    const Piece4 c(threadIdx.x, chunk, a.dim);
+    const uint32_t unit = (c.t / TILE_TOKENS * a.units + c.d / 32) * UNIT_BYTES, t = c.t % TILE_TOKENS, d = c.d % 32;
+    for (uint32_t begin = p.lo / chunk * chunk; begin < p.hi; begin += chunk) {
+        const u32x4* mem = reinterpret_cast<const u32x4*>(in + begin / TILE_TOKENS * tile_bytes);
+        for (uint32_t i = threadIdx.x; i < chunk / TILE_TOKENS * tile_bytes / 16; i += THREADS)
+            *reinterpret_cast<u32x4*>(s_codes + padded_at(i * 16)) = mem[i];
         __syncthreads();
-        const uint32_t from = begin > p.lo ? begin : p.lo, to = umin(begin + TILE_TOKENS, p.hi);
-        const uint32_t n = (to - from) * pieces;
-        for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
-            const uint32_t t = from + i / pieces, d = i % pieces * 8;
-            const uint8_t* unit = s_tile + d / 32 * UNIT_BYTES;
-            Piece<T> v;
+        if (c.real) {
+            u32x2 q[4];
+            if (which == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t at = which == 0 ? key_byte(t % TILE_TOKENS, d % 32) + e : value_byte(t % TILE_TOKENS, d % 32 + e);
-                v.set(e, product((float)(int8_t)unit[at], scale));
+                for (uint32_t j = 0; j < 4; ++j)
+                    q[j] = *reinterpret_cast<const u32x2*>(s_codes + padded_at(unit + key_byte(t + j, d)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        r[e] = *reinterpret_cast<const uint32_t*>(s_codes + padded_at(unit + value_byte(t, d + 4 * i + e)));
+                    const uint32_t a0 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u);
+                    const uint32_t a1 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+                    const uint32_t b0 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+                    const uint32_t b1 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+                    q[0][i] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+                    q[1][i] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+                    q[2][i] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+                    q[3][i] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+                }
             }
-            v.store(out + (uint64_t)(p.row + t - p.lo) * stride + d, a.dim - d);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t at = begin + c.t + j;
+                Piece<T> v;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v.set(e, product((float)(int8_t)(q[j][e / 4] >> (8 * (e % 4))), scale));
+                if (at >= p.lo && at < p.hi) v.store(out + (uint64_t)(p.row + at - p.lo) * stride + c.d, a.dim - c.d);
+            }
         }
         __syncthreads();
     }
@@ -282,7 +416,7 @@ int launch_cache_read_q8(const lecb_cache_q8& c, const lecb_cache_seqs& s, void*
                          void* stream) {
     const uint32_t items = (uint32_t)items_of(c, s);
     // without starts a row may still have no token (length 0)
-    const uint32_t more = s.starts ? (s.tokens + 15) / 16 < 64 ? (s.tokens + 15) / 16 : 64 : (s.seqs + 63) / 64;
+    const uint32_t more = s.starts ? s.tokens / 256 < 64 ? s.tokens / 256 + 1 : 64 : (s.seqs + 63) / 64;
     const ReadArgs a = {seqs_of(c, s), {static_cast<const uint8_t*>(c.k), static_cast<const uint8_t*>(c.v)},
                         {c.k_scale, c.v_scale}, {k, v}, c.heads, c.dim, padded_dim(c.dim) / 32, items, fill};
     return with_float_type(type, [&](auto t) {
