@@ -173,7 +173,7 @@ struct Piece4 {
 // yet behind them) are put together in LDS and stored by 16-byte pieces; where
 // older tokens share the chunk, as in a decoding step, each goes to its own place.
 template <typename T>
-__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 6 : 4) void cache_write_kernel(WriteArgs a) {
+__global__ __launch_bounds__(THREADS) void cache_write_kernel(WriteArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t s_codes[32 * PITCH];
     __shared__ uint32_t s_max[THREADS / 64];
     Span p;
