@@ -14,6 +14,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 __device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline uint32_t of_lane(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ inline float of_lane(float v, int lane) { return __uint_as_float(of_lane(__float_as_uint(v), lane)); }
 
 constexpr int FEW_ROWS = 16, MANY_ROWS = 128;   // of a workgroup, in the two forms
 
@@ -51,10 +53,12 @@ struct AttendArgs {
 struct Item {
     uint32_t seq, rows_at, part, parts, slot, tiles;   // tiles: of each part
     uint32_t first_tile, last_tile;                    // of the sequence
+    uint32_t begin, n, len;                            // its rows, and its tokens with them
 };
 
 struct Load {
     uint32_t first, tiles, rows;   // the tiles that the sequence's rows see, and how many rows by ROWS
+    uint32_t begin, n, len;        // as in Item
 };
 
 template <int ROWS>
@@ -64,9 +68,12 @@ __device__ inline const Form& form_of(const AttendArgs& a) {
 
 template <int ROWS>
 __device__ inline Load load_of(const AttendArgs& a, uint32_t s) {
-    Load l = {0, 0, 0};
+    Load l = {};
     if (s >= a.seqs.seqs) return l;
     const uint32_t n = a.seqs.count(s), len = a.seqs.length(s);
+    l.begin = a.seqs.begin(s);
+    l.n = n;
+    l.len = len;
     if (n == 0 || (n * a.group > a.few) != (ROWS == MANY_ROWS)) return l;   // the other form's
     l.rows = (n * a.group + ROWS - 1) / ROWS;
     if (a.seqs.bad(len) || len == 0) return l;
@@ -93,28 +100,23 @@ __device__ inline uint32_t scan32(uint32_t v, uint32_t lane) {   // of lanes 0 .
     return v;
 }
 
-// Tiles of a part, an even number.
-template <int ROWS>
-__device__ inline uint32_t part_tiles(const AttendArgs& a, uint32_t lane) {
+// The item numbered `w`, found by a wave; false: there are only `slot` of them.
+// With JOIN items are whole rows that were split.  Parts have an even number of tiles.
+template <int ROWS, bool JOIN>
+__device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane, Item& it) {
     const Form& f = form_of<ROWS>(a);
-    uint64_t all = 0;
-    for (uint32_t s0 = 0; s0 < a.seqs.seqs; s0 += 64) {
+    const Load first = load_of<ROWS>(a, lane);   // of the first 64 sequences, all of them in most calls
+    uint64_t all = (uint64_t)first.rows * first.tiles;
+    for (uint32_t s0 = 64; s0 < a.seqs.seqs; s0 += 64) {
         const Load l = load_of<ROWS>(a, s0 + lane);
         all += (uint64_t)l.rows * l.tiles;
     }
     all = sum64(all) * a.heads;
-    const uint64_t part = (all + f.target - 1) / f.target + 1 & ~1ull;
-    return part > f.shortest ? part < 0x7ffffffeu ? (uint32_t)part : 0x7ffffffeu : f.shortest;
-}
-
-// The item numbered `w`, found by a wave; false: there are only `slot` of them.
-// With JOIN items are whole rows that were split.
-template <int ROWS, bool JOIN>
-__device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane, Item& it) {
-    const uint32_t part = part_tiles<ROWS>(a, lane);
+    const uint64_t wish = (all + f.target - 1) / f.target + 1 & ~1ull;
+    const uint32_t part = uniform(wish > f.shortest ? wish < 0x7ffffffeu ? (uint32_t)wish : 0x7ffffffeu : f.shortest);
     uint32_t items = 0, slots = 0;   // of the sequences before
     for (uint32_t s0 = 0; s0 < a.seqs.seqs; s0 += 64) {
-        const Load l = load_of<ROWS>(a, s0 + lane);
+        const Load l = s0 == 0 ? first : load_of<ROWS>(a, s0 + lane);
         const uint32_t parts = l.tiles > part ? (l.tiles + part - 1) / part : 1;
         const uint32_t split = parts > 1 ? l.rows * parts : 0;
         const uint32_t mine = JOIN ? parts > 1 ? l.rows : 0 : l.rows * parts;
@@ -122,19 +124,23 @@ __device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane,
         const uint64_t hit = __ballot(w < upto);
         if (hit) {
             const int at = __builtin_ctzll(hit);
-            const uint32_t k = w - __shfl(upto - mine, at), each = JOIN ? 1 : __shfl(parts, at);
+            const uint32_t k = w - of_lane(upto - mine, at);
             it.seq = uniform(s0 + at);
-            it.parts = uniform(__shfl(parts, at));
-            it.rows_at = uniform(__shfl(l.rows, at) - 1 - k / each);   // the rows that see most come first
-            it.part = uniform(k % each);
-            it.slot = uniform(__shfl(slots_upto - split, at)) + it.rows_at * it.parts + it.part;
-            it.tiles = uniform(part);
-            it.first_tile = uniform(__shfl(l.first, at));
-            it.last_tile = it.first_tile + uniform(__shfl(l.tiles, at));
+            it.parts = of_lane(parts, at);
+            const uint32_t each = JOIN ? 1 : it.parts;
+            it.rows_at = of_lane(l.rows, at) - 1 - k / each;   // the rows that see most come first
+            it.part = k % each;
+            it.slot = of_lane(slots_upto - split, at) + it.rows_at * it.parts + it.part;
+            it.tiles = part;
+            it.first_tile = of_lane(l.first, at);
+            it.last_tile = it.first_tile + of_lane(l.tiles, at);
+            it.begin = of_lane(l.begin, at);
+            it.n = of_lane(l.n, at);
+            it.len = of_lane(l.len, at);
             return true;
         }
-        items = uniform(__shfl(upto, 63));
-        slots = uniform(__shfl(slots_upto, 63));
+        items = of_lane(upto, 63);
+        slots = of_lane(slots_upto, 63);
     }
     it.slot = items;
     return false;
@@ -151,8 +157,8 @@ struct Work {
 
 template <int ROWS>
 __device__ inline bool work_of(const AttendArgs& a, const Item& it, uint32_t h, Work& k) {
-    const uint32_t n = uniform(a.seqs.count(it.seq)), len = uniform(a.seqs.length(it.seq));
-    k.begin = uniform(a.seqs.begin(it.seq));
+    const uint32_t n = it.n, len = it.len;
+    k.begin = it.begin;
     k.rows = n * a.group;
     k.slot = it.slot * a.heads + h;
     k.parts = it.parts;
@@ -262,8 +268,6 @@ __device__ inline float scale_exponent(float s) {
     return (float)(s == 0.0f ? SCALE_LOW : e > SCALE_LOW ? e : SCALE_LOW);
 }
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ inline uint32_t of_lane(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-__device__ inline float of_lane(float v, int lane) { return __uint_as_float(of_lane(__float_as_uint(v), lane)); }
 // The largest of the lanes 32 apart, and of those 16 apart.
 __device__ inline float max_of_halves(float v) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -275,29 +279,48 @@ __device__ inline float max_of_quarters(float v) {
 }
 __device__ inline float inf() { return __uint_as_float(0x7f800000u); }
 
-// One row of q as operands: N pieces of eight dimensions, d0 + step i and on; the
-// lanes that share a row are LANES apart.  Returns what takes a product of codes to a score.
+// Rows of q into LDS, `pitch` elements apart, zeros past the head's dimensions and
+// past the last row: what all waves of a workgroup then take their operands from.
+template <typename T>
+__device__ inline void stage_rows(const AttendArgs& a, const Work& k, uint32_t h, uint32_t rows, uint32_t pitch, T* to) {
+    typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
+    typedef piece loose __attribute__((aligned(sizeof(T))));
+    constexpr uint32_t N = 16 / sizeof(T);
+    const uint32_t across = pitch / N;
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < rows * across; i += blockDim.x) {
+        const uint32_t row = k.r0 + i / across, d = i % across * N;
+        const T* p = reinterpret_cast<const T*>(a.q) + (uint64_t)(k.begin + row / a.group) * a.q_token +
+                     (uint64_t)(h * a.group + row % a.group) * a.q_head + d;
+        piece x = {};
+        if (row < k.rows && d < a.dim) {
+            if (d + N <= a.dim) {
+                x = *reinterpret_cast<const loose*>(p);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < N; ++e)
+                    if (d + e < a.dim) x[e] = p[e];
+            }
+        }
+        *reinterpret_cast<piece*>(to + i * N) = x;
+    }
+}
+
+// One row as operands: N pieces of eight dimensions, d0 + step i and on; the lanes
+// that share a row are LANES apart.  Returns what takes a product of codes to a score.
 template <typename T, int N, int LANES>
-__device__ inline float load_row(const AttendArgs& a, const Work& k, uint32_t row, uint32_t h, uint32_t d0, uint32_t step,
-                                 f16x8 (&q)[N][Parts<T>::Q]) {
-    const bool real = row < k.rows;
-    const uint32_t token = real ? row / a.group : 0, head = real ? row % a.group : 0;
-    const T* p = reinterpret_cast<const T*>(a.q) + (real ? (uint64_t)(k.begin + token) * a.q_token : 0) +
-                 (uint64_t)(h * a.group + head) * a.q_head;
-    Piece<T> x[N];
+__device__ inline float load_row(const AttendArgs& a, const T* row, uint32_t d0, uint32_t step, f16x8 (&q)[N][Parts<T>::Q]) {
+    typedef T piece __attribute__((ext_vector_type(8)));
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-        const uint32_t d = step * u + d0, count = real && d < a.dim ? a.dim - d : 0;
-        x[u].load(p + (count ? d : 0), count);
-    }
-#pragma unroll
-    for (int u = 0; u < N; ++u)
+        const piece x = *reinterpret_cast<const piece*>(row + step * u + d0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint32_t b = __float_as_uint(x[u][e]) & 0x7fffffffu;
+            const uint32_t b = __float_as_uint((float)x[e]) & 0x7fffffffu;
             top = b > top ? b : top;
         }
+    }
 #pragma unroll
     for (int o = LANES; o < 64; o <<= 1) {
         const uint32_t b = __shfl_xor(top, o);
@@ -306,17 +329,35 @@ __device__ inline float load_row(const AttendArgs& a, const Work& k, uint32_t ro
     int lift = 0;
     if (Parts<T>::LIFT && top != 0) lift = 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top));
 #pragma unroll
-    for (int u = 0; u < N; ++u)
+    for (int u = 0; u < N; ++u) {
+        const piece x = *reinterpret_cast<const piece*>(row + step * u + d0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float f = Parts<T>::LIFT ? ldexpf(x[u][e], lift) : x[u][e];
+            float f = Parts<T>::LIFT ? ldexpf((float)x[e], lift) : (float)x[e];
 #pragma unroll
             for (int j = 0; j < Parts<T>::Q; ++j) {
                 q[u][j][e] = (_Float16)f;
                 f -= (float)q[u][j][e];
             }
         }
+    }
     return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : ldexpf(a.scale, -lift);
+}
+
+// Four neighbouring results, as far as the head's dimensions go.
+template <typename T>
+__device__ inline void put_four(const AttendArgs& a, const Work& k, uint32_t h, uint32_t row, uint32_t d, const T (&v)[4]) {
+    typedef T four __attribute__((ext_vector_type(4)));
+    typedef four loose __attribute__((aligned(sizeof(T))));
+    T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + row / a.group) * a.out_token +
+           (uint64_t)(h * a.group + row % a.group) * a.out_head + d;
+    if (d + 4 <= a.dim) {
+        *reinterpret_cast<loose*>(o) = four{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 3; ++e)
+            if (d + e < a.dim) o[e] = v[e];
+    }
 }
 
 }  // namespace lecb

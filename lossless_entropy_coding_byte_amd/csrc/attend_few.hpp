@@ -6,28 +6,6 @@
 #if defined(__HIPCC__)
 namespace lecb {
 
-// A tile of 32 tokens, in registers as it lies.
-template <int U>
-struct Tile {
-    u32x4 k[U], v[U];
-    float scales;   // of keys in even lanes, of values in odd ones
-    bool none;      // the table names no block of the cache
-    __device__ void load(const AttendArgs& a, uint32_t page, uint32_t t, uint32_t shift, uint32_t h, uint32_t lane) {
-        none = page >= a.seqs.blocks;
-        const uint64_t cell = (uint64_t)(none ? 0 : page) * a.heads + h;
-        const uint64_t at = ((cell << shift) + (t & ((1u << shift) - 1))) * (U * UNIT_BYTES) + lane * 16;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            k[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.k + at + u * UNIT_BYTES));
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.v + at + u * UNIT_BYTES));
-        scales = (lane & 1 ? a.v_scale : a.k_scale)[cell];
-    }
-    __device__ float k_scale() const { return none ? __uint_as_float(0x7fc00000u) : of_lane(scales, 0); }
-    __device__ float v_scale() const { return of_lane(scales, 1); }
-};
-
 // Few rows: a workgroup takes 16 NT rows of one head over a part of the tiles,
 // its waves tile by tile in turn, each with a softmax of its own; their sums are
 // joined at the end.  Matrix instructions by 16 x 16 x 32, transposed: codes of
@@ -35,14 +13,17 @@ struct Tile {
 // scores stand in one lane of each 16, four tokens each, and are the second
 // product's operand as they are; values are stored in that order of tokens.
 // Neither codes nor scores go through LDS.
-template <int NT, int WAVES>
+template <typename T, int U, int NT, int WAVES>
 struct FewMemory {
-    float sum[WAVES][16 * NT][68];
+    union {
+        T q[16 * NT][32 * U];
+        float sum[WAVES][16 * NT][68];
+    };
     float ref[WAVES][16 * NT], l[WAVES][16 * NT];
 };
 
 template <typename T, int U, int NT, int WAVES>
-__device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<NT, WAVES>& mem) {
+__device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<T, U, NT, WAVES>& mem) {
     constexpr int ROWS = 16 * NT, NQ = Parts<T>::Q, NP = Parts<T>::P, THREADS = 64 * WAVES;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     Work k;
@@ -51,7 +32,43 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         bad_rows<T>(a, k, h);
         return;
     }
-    const uint32_t seq = it.seq;
+    const uint32_t seq = it.seq, shift = __builtin_ctz(a.seqs.block / TILE_TOKENS);
+    const int from = k.from, to = k.to, lo_most = k.lo_most, hi_least = k.hi_least;
+
+    // a tile's codes as they lie and, in even and odd lanes, the scales of its keys and values
+    u32x4 kc[U], vc[U];
+    float scales = 0.0f;
+    bool none = false, none_next = false;   // the table names no block of the cache
+    auto page = [&](int t) { return a.seqs.page(seq, (uint32_t)t >> shift); };
+    auto cell_of = [&](uint32_t found) {
+        const uint32_t page = uniform(found);
+        none_next = page >= a.seqs.blocks;
+        return (uint64_t)(none_next ? 0 : page) * a.heads + h;
+    };
+    auto place = [&](uint64_t cell, int t) {
+        return ((cell << shift) + ((uint32_t)t & ((1u << shift) - 1))) * (U * UNIT_BYTES) + lane * 16;
+    };
+    auto load_codes = [&](const uint8_t* codes, uint64_t at, u32x4 (&w)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + at + u * UNIT_BYTES));
+    };
+    auto load_scales = [&](uint64_t cell) { return (lane & 1 ? a.v_scale : a.k_scale)[cell]; };
+    auto next_of = [&](int t) { return t + WAVES < to ? t + WAVES : t; };
+
+    // the first tile is on its way while the rows are made ready
+    int t = from + (int)wave;
+    uint32_t found = 0;
+    if (t < to) {
+        const uint32_t first = page(t);
+        found = page(next_of(t));
+        const uint64_t cell = cell_of(first), at = place(cell, t);
+        none = none_next;
+        load_codes(a.k, at, kc);
+        load_codes(a.v, at, vc);
+        scales = load_scales(cell);
+    }
+    stage_rows(a, k, h, ROWS, 32 * U, &mem.q[0][0]);
+    __syncthreads();
 
     // rows: lane r of each 16 has row r of each 16, dimensions 32 u + 8 g and on
     f16x8 q[NT][U][NQ];
@@ -60,12 +77,11 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const uint32_t row = k.r0 + 16 * c + r;
-        factor[c] = load_row<T, U, 16>(a, k, row, h, 8 * g, 32, q[c]);
+        factor[c] = load_row<T, U, 16>(a, mem.q[16 * c + r], 8 * g, 32, q[c]);
         const int at = k.old + (row < k.rows ? (int)(row / a.group) : 0);
         hi[c] = a.causal ? at : k.len - 1;
         lo[c] = a.window ? at - (int)a.window + 1 : 0;
     }
-    const int from = k.from, to = k.to, lo_most = k.lo_most, hi_least = k.hi_least;
 
     f32x4 acc[NT][2 * U];
     float ref[NT], sum[NT];
@@ -76,9 +92,13 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
 #pragma unroll
         for (int i = 0; i < 2 * U; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const uint32_t shift = __builtin_ctz(a.seqs.block / TILE_TOKENS);
 
-    auto compute = [&](int t, const Tile<U>& x) {
+    // Codes have one set of registers: the next tile's keys are asked for once this one's are
+    // operands, its values after theirs, its block one tile ahead.  Past the last tile the
+    // same one is loaded again.
+    for (; t < to; t += WAVES) {
+        const int t1 = next_of(t), at = t * (int)TILE_TOKENS;
+        const float ks = none ? __uint_as_float(0x7fc00000u) : of_lane(scales, 0), vs = of_lane(scales, 1);
         f32x4 s[NT][2];
 #pragma unroll
         for (int c = 0; c < NT; ++c) s[c][0] = s[c][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -86,19 +106,23 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const f16x8 codes = operand(x.k[u][2 * b], x.k[u][2 * b + 1]);
+                const f16x8 codes = operand(kc[u][2 * b], kc[u][2 * b + 1]);
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
 #pragma unroll
                     for (int j = 0; j < NQ; ++j)
                         s[c][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, q[c][u][j], s[c][b], 0, 0, 0);
             }
-        const float ks = x.k_scale(), vs = x.v_scale(), unit = scale_exponent(vs);
-        const int at = t * (int)TILE_TOKENS;
+        const uint64_t cell = cell_of(found), next_at = place(cell, t1);
+        load_codes(a.k, next_at, kc);
+        scales = load_scales(cell);
+        none = none_next;
+        found = page(next_of(t1));
+
         // all rows see all of the tile's tokens, and the larger product is the larger score
         const bool plain = at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f;
         const bool number = fabsf(vs) < inf();
-        const float down = number ? vs * P_DOWN : 0.0f;
+        const float down = number ? vs * P_DOWN : 0.0f, unit = scale_exponent(vs);
         f16x8 p[NT][NP];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
@@ -146,37 +170,16 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const f16x8 codes = operand(x.v[u][2 * b], x.v[u][2 * b + 1]);
+                const f16x8 codes = operand(vc[u][2 * b], vc[u][2 * b + 1]);
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
 #pragma unroll
                     for (int j = 0; j < NP; ++j)
                         acc[c][2 * u + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, p[c][j], acc[c][2 * u + b], 0, 0, 0);
             }
-    };
-    int t = from + (int)wave;
-    if (t < to) {
-        // the next tile's loads are in flight while one is worked on, its block's number one more ahead;
-        // past the last tile the same one is asked for again
-        Tile<U> x, y;
-        auto page = [&](int i) { return uniform(a.seqs.page(seq, (uint32_t)(i < to ? i : t) >> shift)); };
-        x.load(a, page(t), t, shift, h, lane);
-        uint32_t ahead = page(t + WAVES);
-        while (true) {
-            int next = t + WAVES < to ? t + WAVES : t;
-            y.load(a, ahead, next, shift, h, lane);
-            ahead = page(t + 2 * WAVES);
-            compute(t, x);
-            t += WAVES;
-            if (t >= to) break;
-            next = t + WAVES < to ? t + WAVES : t;
-            x.load(a, ahead, next, shift, h, lane);
-            ahead = page(t + 2 * WAVES);
-            compute(t, y);
-            t += WAVES;
-            if (t >= to) break;
-        }
+        load_codes(a.v, next_at, vc);
     }
+    __syncthreads();   // the rows in LDS are no longer needed
 
     // the waves' sums, joined in their order
 #pragma unroll
@@ -209,8 +212,8 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
                     *reinterpret_cast<f32x4*>(&mem.sum[wave][16 * c + r][16 * i + 4 * g]) = acc[c][2 * d0 + i];
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < ROWS * 16; i += THREADS) {
-            const uint32_t row = i / 16, d = i % 16 * 4;
-            if (row >= k.have) break;
+            const uint32_t row = i / 16, d = i % 16 * 4, at = 32 * d0 + d;
+            if (row >= k.have || at >= 32 * U) continue;
             f32x4 v = *reinterpret_cast<const f32x4*>(&mem.sum[0][row][d]);
 #pragma unroll
             for (int j = 1; j < WAVES; ++j) v += *reinterpret_cast<const f32x4*>(&mem.sum[j][row][d]);
@@ -219,21 +222,16 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
             for (int j = 1; j < WAVES; ++j) least = fminf(least, mem.ref[j][row]);
 #pragma unroll
             for (int j = 0; j < WAVES; ++j) l += mem.l[j][row] * (mem.ref[j][row] == least ? 1.0f : exp2_of(least - mem.ref[j][row]));
-            const uint32_t at = 32 * d0 + d;
             if (k.parts > 1) {
-                if (at < 32 * U) *reinterpret_cast<f32x4*>(ws + row * (32 * U + 4) + 4 + at) = v;
+                *reinterpret_cast<f32x4*>(ws + row * (32 * U + 4) + 4 + at) = v;
                 if (at == 0) {
                     ws[row * (32 * U + 4)] = least;
                     ws[row * (32 * U + 4) + 1] = l;
                 }
             } else {
                 const float up = l == 0.0f ? 0.0f : OUT / l;
-                const uint32_t i = k.r0 + row;
-                T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + i / a.group) * a.out_token +
-                       (uint64_t)(h * a.group + i % a.group) * a.out_head + at;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (at + j < a.dim) o[j] = (T)(v[j] * up);
+                const T o[4] = {(T)(v[0] * up), (T)(v[1] * up), (T)(v[2] * up), (T)(v[3] * up)};
+                put_four(a, k, h, k.r0 + row, at, o);
             }
         }
         __syncthreads();

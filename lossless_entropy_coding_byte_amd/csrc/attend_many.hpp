@@ -45,14 +45,19 @@ struct Scales {
 // rows: a row's scores stand in two lanes, which is the second product's operand,
 // with tokens 16 m + 8 (i / 4) + 4 (lane / 32) + i % 4 as its eight, so the
 // values' operands are put together in that order.
-template <int U>
+template <typename T, int U>
 struct ManyMemory {
-    uint8_t k[2][2][2 * U][UNIT_BYTES];    // [buffer][tile][16 dimensions]
-    uint8_t v[2][2][U][2][UNIT_BYTES];     // [buffer][tile][32 dimensions][16 tokens]
+    union {
+        struct {
+            uint8_t k[2][2][2 * U][UNIT_BYTES];    // [buffer][tile][16 dimensions]
+            uint8_t v[2][2][U][2][UNIT_BYTES];     // [buffer][tile][32 dimensions][16 tokens]
+        };
+        T rows[MANY_ROWS][32 * U];   // queries before, results after
+    };
 };
 
 template <typename T, int U>
-__device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t h, ManyMemory<U>& mem) {
+__device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t h, ManyMemory<T, U>& mem) {
     constexpr int ROWS = MANY_ROWS, NQ = Parts<T>::Q, NP = Parts<T>::P;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, hh = lane >> 5;
     Work k;
@@ -67,7 +72,10 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     const uint32_t row = k.r0 + 32 * wave + r;
     const bool real = row < k.rows;
     f16x8 q[2 * U][NQ];
-    const float factor = load_row<T, 2 * U, 32>(a, k, row, h, 8 * hh, 16, q);
+    stage_rows(a, k, h, ROWS, 32 * U, &mem.rows[0][0]);
+    __syncthreads();
+    const float factor = load_row<T, 2 * U, 32>(a, mem.rows[32 * wave + r], 8 * hh, 16, q);
+    __syncthreads();
     const int at_token = k.old + (real ? (int)(row / a.group) : 0);
     const int hi = a.causal ? at_token : k.len - 1, lo = a.window ? at_token - (int)a.window + 1 : 0;
     // tiles go by pairs: what a pair has too many is masked
@@ -217,8 +225,8 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     }
 
     sum += __shfl_xor(sum, 32);
-    if (!real) return;
     if (k.parts > 1) {
+        if (!real) return;
         float* ws = form_of<ROWS>(a).ws + ((uint64_t)k.slot * ROWS + 32 * wave + r) * (32 * U + 4);
         if (hh == 0) {
             ws[0] = ref;
@@ -230,19 +238,24 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<f32x4*>(ws + 4 + 32 * u + 8 * j + 4 * hh) =
                     f32x4{acc[u][4 * j], acc[u][4 * j + 1], acc[u][4 * j + 2], acc[u][4 * j + 3]};
-    } else {
-        const float up = sum == 0.0f ? 0.0f : OUT / sum;
-        T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + row / a.group) * a.out_token +
-               (uint64_t)(h * a.group + row % a.group) * a.out_head;
+        return;
+    }
+    // through LDS, so that rows leave whole
+    typedef T four __attribute__((ext_vector_type(4)));
+    const float up = sum == 0.0f ? 0.0f : OUT / sum;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t d = 32 * u + 8 * j + 4 * hh;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (d + e < a.dim) o[d + e] = (T)(acc[u][4 * j + e] * up);
-            }
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<four*>(&mem.rows[32 * wave + r][32 * u + 8 * j + 4 * hh]) =
+                four{(T)(acc[u][4 * j] * up), (T)(acc[u][4 * j + 1] * up), (T)(acc[u][4 * j + 2] * up), (T)(acc[u][4 * j + 3] * up)};
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < k.have * (8 * U); i += blockDim.x) {
+        const uint32_t row = i / (8 * U), d = i % (8 * U) * 4;
+        if (d >= a.dim) continue;
+        const four x = *reinterpret_cast<const four*>(&mem.rows[row][d]);
+        const T o[4] = {x[0], x[1], x[2], x[3]};
+        put_four(a, k, h, k.r0 + row, d, o);
     }
 }
 

@@ -17,8 +17,8 @@ constexpr bool HAS_MANY = sizeof(T) == 2 || U < 8;
 // A workgroup takes one item.  Those of the first launch without one see to the
 // rows of no sequence.
 template <typename T, int U>
-__global__ __launch_bounds__(THREADS, U <= 4 && U * sizeof(T) < 16 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
-    __shared__ __attribute__((aligned(16))) FewMemory<1, WAVES> memory;
+__global__ __launch_bounds__(THREADS, U * sizeof(T) <= 16 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
+    __shared__ __attribute__((aligned(16))) FewMemory<T, U, 1, WAVES> memory;
     const uint32_t h = blockIdx.x % a.heads, w = blockIdx.x / a.heads;
     Item it;
     if (find_item<FEW_ROWS, false>(a, w, threadIdx.x & 63, it))
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(THREADS, U <= 4 && U * sizeof(T) < 16 ? 2 : 1) void
 
 template <typename T, int U>
 __global__ __launch_bounds__(THREADS, U <= 4 && U * sizeof(T) < 16 ? 2 : 1) void attend_many_kernel(AttendArgs a) {
-    __shared__ __attribute__((aligned(16))) ManyMemory<U> memory;
+    __shared__ __attribute__((aligned(16))) ManyMemory<T, U> memory;
     const uint32_t h = blockIdx.x % a.heads, w = blockIdx.x / a.heads;
     Item it;
     if (find_item<MANY_ROWS, false>(a, w, threadIdx.x & 63, it))
@@ -94,12 +94,8 @@ __device__ inline void join(const AttendArgs& a, const Item& it, uint32_t h, uin
         }
         if (share == 0 && group < GROUPS && row < k.have) {
             const float up = l == 0.0f ? 0.0f : OUT / l;
-            const uint32_t i = k.r0 + row;
-            T* o = reinterpret_cast<T*>(a.out) + (uint64_t)(k.begin + i / a.group) * a.out_token +
-                   (uint64_t)(h * a.group + i % a.group) * a.out_head + d;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (d + j < a.dim) o[j] = (T)(v[j] * up);
+            const T o[4] = {(T)(v[0] * up), (T)(v[1] * up), (T)(v[2] * up), (T)(v[3] * up)};
+            put_four(a, k, h, k.r0 + row, d, o);
         }
     }
 }
@@ -138,7 +134,8 @@ Shape shape_of(bool many, uint32_t heads, uint32_t group, uint32_t block, uint64
     if (!many && seqs * tiles_of(few, rows) < most) most = seqs * tiles_of(few, rows);
     const uint64_t parts = tiles_of(width * block / TILE_TOKENS + 2, s.shortest);
     const bool split = parts > 1;
-    s.items = most + (split ? s.target / heads : 0) + 1;   // one without an item, for the rows of no sequence
+    s.items = split ? s.target / heads < most * (parts - 1) ? most + s.target / heads : most * parts : most;
+    s.items += 1;   // one without an item, for the rows of no sequence
     s.joins = split ? s.target / heads < most ? s.target / heads : most : 0;
     s.slots = split ? 2ull * s.target : 0;
     if (split && most * heads * parts < s.slots) s.slots = most * heads * parts;
