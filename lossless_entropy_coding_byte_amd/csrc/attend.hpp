@@ -83,19 +83,19 @@ __device__ inline Load load_of(const AttendArgs& a, uint32_t s) {
     return l;
 }
 
-__device__ inline uint64_t sum64(uint64_t v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
+// Over lanes 0 .. limit - 1 (a power of two), the others holding zeros.
+__device__ inline uint64_t sum64(uint64_t v, uint32_t limit) {
+    for (uint32_t o = 1; o < limit; o <<= 1) {
         const uint32_t lo = __shfl_xor((uint32_t)v, o), hi = __shfl_xor((uint32_t)(v >> 32), o);
         v += (uint64_t)hi << 32 | lo;
     }
-    return v;
+    return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
 }
-__device__ inline uint32_t scan32(uint32_t v, uint32_t lane) {   // of lanes 0 .. lane
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
+// For lane i the sum of lanes 0 .. i.
+__device__ inline uint32_t scan32(uint32_t v, uint32_t lane, uint32_t limit) {
+    for (uint32_t o = 1; o < limit; o <<= 1) {
         const uint32_t b = __shfl_up(v, o);
-        v += lane >= (uint32_t)o ? b : 0;
+        v += lane >= o ? b : 0;
     }
     return v;
 }
@@ -111,8 +111,10 @@ __device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane,
         const Load l = load_of<ROWS>(a, s0 + lane);
         all += (uint64_t)l.rows * l.tiles;
     }
-    all = sum64(all) * a.heads;
-    const uint64_t wish = (all + f.target - 1) / f.target + 1 & ~1ull;
+    uint32_t limit = 1;   // lanes that hold something
+    while (limit < 64 && limit < a.seqs.seqs) limit *= 2;
+    all = sum64(all, limit) * a.heads + f.target - 1;
+    const uint64_t wish = (all >> 32 ? all / f.target : (uint32_t)all / f.target) + 1 & ~1ull;
     const uint32_t part = uniform(wish > f.shortest ? wish < 0x7ffffffeu ? (uint32_t)wish : 0x7ffffffeu : f.shortest);
     uint32_t items = 0, slots = 0;   // of the sequences before
     for (uint32_t s0 = 0; s0 < a.seqs.seqs; s0 += 64) {
@@ -120,7 +122,7 @@ __device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane,
         const uint32_t parts = l.tiles > part ? (l.tiles + part - 1) / part : 1;
         const uint32_t split = parts > 1 ? l.rows * parts : 0;
         const uint32_t mine = JOIN ? parts > 1 ? l.rows : 0 : l.rows * parts;
-        const uint32_t upto = scan32(mine, lane) + items, slots_upto = scan32(split, lane) + slots;
+        const uint32_t upto = scan32(mine, lane, limit) + items, slots_upto = scan32(split, lane, limit) + slots;
         const uint64_t hit = __ballot(w < upto);
         if (hit) {
             const int at = __builtin_ctzll(hit);
@@ -139,8 +141,8 @@ __device__ inline bool find_item(const AttendArgs& a, uint32_t w, uint32_t lane,
             it.len = of_lane(l.len, at);
             return true;
         }
-        items = of_lane(upto, 63);
-        slots = of_lane(slots_upto, 63);
+        items = of_lane(upto, limit - 1);
+        slots = of_lane(slots_upto, limit - 1);
     }
     it.slot = items;
     return false;

@@ -116,18 +116,21 @@ __global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a, uint
 }
 
 // What a form's work may come to, whatever the lengths are.  Workgroups wished for
-// are as many as the GPU holds at once; a part has `shortest` tiles at least.
+// are as many as the GPU holds at once; a part has `shortest` tiles at least: one for
+// each wave of the form for few rows where a tile is short work (one token after 1000 in 128
+// dimensions 10.4 us, with two 11.2), two where it is not (8 sequences with windows of 4096 in
+// 256 dimensions 16.8 us, with one 19.3).
 struct Shape {
     uint64_t items, joins;   // for each head: workgroups, rows that are split
     uint64_t slots;          // of all heads
     uint32_t target, shortest;
 };
-Shape shape_of(bool many, uint32_t heads, uint32_t group, uint32_t block, uint64_t seqs, uint64_t tokens, uint64_t width,
+Shape shape_of(bool many, uint32_t dim, uint32_t heads, uint32_t group, uint32_t block, uint64_t seqs, uint64_t tokens, uint64_t width,
                uint64_t few) {
     const uint64_t rows = many ? MANY_ROWS : FEW_ROWS;
     Shape s;
     s.target = (uint32_t)((many ? 2 : 4) * device_cu_count());
-    s.shortest = many ? 16 : 8;
+    s.shortest = many ? 16 : dim <= 128 ? 4 : 8;
     // a sequence's rows, rounded up; none has more than `few` in the form for few
     uint64_t most = tokens * group / rows + seqs;
     if (tokens * tiles_of(group, rows) < most) most = tokens * tiles_of(group, rows);
@@ -201,7 +204,7 @@ uint64_t attention_q8_workspace(const lecb_cache_q8& c, uint64_t seqs, uint64_t 
     const uint32_t group = heads / c.heads;
     uint64_t bytes = 0;
     for (int many = 0; many < 2; ++many)
-        bytes += bytes_of(shape_of(many, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group)),
+        bytes += bytes_of(shape_of(many, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group)),
                           many, c.dim);
     return bytes;
 }
@@ -218,7 +221,7 @@ int launch_attention_q8(const AttentionQ8& x, void* stream) {
     Shape shape[2];
     float* ws = static_cast<float*>(x.ws);
     for (int i = 0; i < 2; ++i) {
-        shape[i] = shape_of(i, a.heads, group, x.cache.block, x.seqs.seqs, x.seqs.tokens, x.seqs.width, most);
+        shape[i] = shape_of(i, a.dim, a.heads, group, x.cache.block, x.seqs.seqs, x.seqs.tokens, x.seqs.width, most);
         a.form[i] = {ws, shape[i].target, shape[i].shortest, (uint32_t)shape[i].slots};
         ws += bytes_of(shape[i], i, x.cache.dim) / sizeof(float);
     }
