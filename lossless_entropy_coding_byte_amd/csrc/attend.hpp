@@ -17,7 +17,7 @@ __device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfir
 __device__ inline uint32_t of_lane(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ inline float of_lane(float v, int lane) { return __uint_as_float(of_lane(__float_as_uint(v), lane)); }
 
-constexpr int FEW_ROWS = 16, MANY_ROWS = 128;   // of a workgroup, in the two forms
+constexpr int FEW_ROWS = 16;   // of a workgroup in the form for few rows; in that for many 128 or 256
 
 // How one form's work is shared out.  A sequence's rows (tokens x query heads of
 // one head of the cache) go by ROWS at a time, and the tiles that they see are
@@ -63,7 +63,7 @@ struct Load {
 
 template <int ROWS>
 __device__ inline const Form& form_of(const AttendArgs& a) {
-    return a.form[ROWS == MANY_ROWS];
+    return a.form[ROWS != FEW_ROWS];
 }
 
 template <int ROWS>
@@ -74,7 +74,7 @@ __device__ inline Load load_of(const AttendArgs& a, uint32_t s) {
     l.begin = a.seqs.begin(s);
     l.n = n;
     l.len = len;
-    if (n == 0 || (n * a.group > a.few) != (ROWS == MANY_ROWS)) return l;   // the other form's
+    if (n == 0 || (n * a.group > a.few) != (ROWS != FEW_ROWS)) return l;   // the other form's
     l.rows = (n * a.group + ROWS - 1) / ROWS;
     if (a.seqs.bad(len) || len == 0) return l;
     const uint32_t at = len > n ? len - n : 0;
@@ -261,13 +261,14 @@ struct Parts<float> {
 // nearly each pair of tiles without that, once or twice with it.
 constexpr float REF_TOP = 30.0f, LAG = 4.0f;
 constexpr float P_DOWN = 0x1p-19f;   // into halves: at most 2^(30 + LAG - 19)
+constexpr float P_DOWN_LOG2 = -19.0f;
 constexpr float OUT = 0x1p19f;       // and back
 constexpr int SCALE_LOW = -60;
 
 __device__ inline float scale_exponent(float s) {
-    // infinities and NaN give 0, and zero the lowest: all that counts is that p stays finite
+    // infinities and NaN give 0, and so does zero: all that counts is that p stays finite
     const int e = __builtin_amdgcn_frexp_expf(s);
-    return (float)(s == 0.0f ? SCALE_LOW : e > SCALE_LOW ? e : SCALE_LOW);
+    return (float)(e > SCALE_LOW ? e : SCALE_LOW);
 }
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // The largest of the lanes 32 apart, and of those 16 apart.

@@ -6,59 +6,33 @@
 #if defined(__HIPCC__)
 namespace lecb {
 
-// A wave's part of a step of two tiles: wave w loads the units of one tile's keys
-// (w < 2) or values.
-template <int U>
-struct Part {
-    u32x4 w[U];
-    float scales;      // of the tiles' keys in lanes 0 and 1, of their values in 2 and 3
-    uint32_t pages;    // of the tiles, in even and odd lanes: 0xffffffff where there is none
-    __device__ void load(const AttendArgs& a, uint32_t found, uint32_t t, uint32_t shift, uint32_t h, uint32_t wave,
-                         uint32_t lane) {
-        pages = found;
-        const uint32_t page = of_lane(found, wave & 1), mine = found < a.seqs.blocks ? found : 0;
-        const uint64_t cell = (uint64_t)(page < a.seqs.blocks ? page : 0) * a.heads + h;
-        const uint64_t at = ((cell << shift) + ((t + (wave & 1)) & ((1u << shift) - 1))) * (U * UNIT_BYTES) + lane * 16;
-        const uint8_t* codes = wave < 2 ? a.k : a.v;
-#pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const u32x4*>(codes + at + u * UNIT_BYTES);
-        scales = (lane & 2 ? a.v_scale : a.k_scale)[(uint64_t)mine * a.heads + h];
-    }
-};
-struct Scales {
-    float k[2], v[2];
-    template <int U>
-    __device__ void set(const AttendArgs& a, const Part<U>& x) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            k[i] = of_lane(x.pages, i) < a.seqs.blocks ? of_lane(x.scales, i) : __uint_as_float(0x7fc00000u);
-            v[i] = of_lane(x.scales, 2 + i);
-        }
-    }
-};
-
-// Many rows: a workgroup takes 128 rows of one head, 32 a wave, over a part of the
-// tiles, two at a time.  Their codes are turned into halves once, by all waves, and
-// put into LDS as matrix operands of 1 KiB: of keys for 32 tokens x 16
+// Many rows: a workgroup takes 32 rows of one head a wave over a part of the
+// tiles, two at a time.  Their codes are turned into halves once, by all waves,
+// and put into LDS as matrix operands of 1 KiB: of keys for 32 tokens x 16
 // dimensions, of values for 32 dimensions x 16 tokens, each in the order of the
 // lanes.  Matrix instructions by 32 x 32 x 16, transposed as in the form for few
 // rows: a row's scores stand in two lanes, which is the second product's operand,
 // with tokens 16 m + 8 (i / 4) + 4 (lane / 32) + i % 4 as its eight, so the
 // values' operands are put together in that order.
 template <typename T, int U>
+constexpr int MANY_WAVES = U <= 4 && U != 3 && sizeof(T) == 2 ? 8 : 4;
+template <typename T, int U>
+constexpr int MANY_ROWS = 32 * MANY_WAVES<T, U>;
+
+template <typename T, int U>
 struct ManyMemory {
     union {
         struct {
             uint8_t k[2][2][2 * U][UNIT_BYTES];    // [buffer][tile][16 dimensions]
-            uint8_t v[2][2][U][2][UNIT_BYTES];     // [buffer][tile][32 dimensions][16 tokens]
+            uint8_t v[3][2][U][2][UNIT_BYTES];     // [buffer][tile][32 dimensions][16 tokens]
         };
-        T rows[MANY_ROWS][32 * U];   // queries before, results after
+        T rows[MANY_ROWS<T, U>][32 * U];   // queries before, results after
     };
 };
 
 template <typename T, int U>
 __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t h, ManyMemory<T, U>& mem) {
-    constexpr int ROWS = MANY_ROWS, NQ = Parts<T>::Q, NP = Parts<T>::P;
+    constexpr int WAVES = MANY_WAVES<T, U>, ROWS = MANY_ROWS<T, U>, SHARE = 4 * U / WAVES, NC = 1, NQ = Parts<T>::Q, NP = Parts<T>::P;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, hh = lane >> 5;
     Work k;
     if (!work_of<ROWS>(a, it, h, k)) return;
@@ -68,187 +42,271 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     }
     const uint32_t seq = it.seq;
 
-    // rows: lane r of each 32 has row r of the wave's, dimensions 16 e + 8 hh and on
-    const uint32_t row = k.r0 + 32 * wave + r;
-    const bool real = row < k.rows;
-    f16x8 q[2 * U][NQ];
+    // rows: lane r of each 32 has row r of each of the wave's 32, dimensions 16 e + 8 hh and on
     stage_rows(a, k, h, ROWS, 32 * U, &mem.rows[0][0]);
     __syncthreads();
-    const float factor = load_row<T, 2 * U, 32>(a, mem.rows[32 * wave + r], 8 * hh, 16, q);
+    f16x8 q[NC][2 * U][NQ];
+    float factor[NC];
+    int hi[NC], lo[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const uint32_t i = 32 * (WAVES * c + wave) + r, row = k.r0 + i;
+        factor[c] = load_row<T, 2 * U, 32>(a, mem.rows[i], 8 * hh, 16, q[c]);
+        const int at = k.old + (row < k.rows ? (int)(row / a.group) : 0);
+        hi[c] = a.causal ? at : k.len - 1;
+        lo[c] = a.window ? at - (int)a.window + 1 : 0;
+    }
     __syncthreads();
-    const int at_token = k.old + (real ? (int)(row / a.group) : 0);
-    const int hi = a.causal ? at_token : k.len - 1, lo = a.window ? at_token - (int)a.window + 1 : 0;
     // tiles go by pairs: what a pair has too many is masked
     const int from = k.from, to = k.to, lo_most = k.lo_most, hi_least = k.hi_least;
     const uint32_t shift = __builtin_ctz(a.seqs.block / TILE_TOKENS);
 
-    f32x16 acc[U];
+    f32x16 acc[NC][U];
+    float ref[NC], sum[NC];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int c = 0; c < NC; ++c) {
+        ref[c] = inf();
+        sum[c] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
-    float ref = inf(), sum = 0.0f;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c][u][i] = 0.0f;
+    }
 
-    // the blocks of tiles t and t + 1, in even and odd lanes
+    // the blocks of a step's tiles t and t + 1, in even and odd lanes
     auto pages = [&](int t) { return a.seqs.page(seq, ((uint32_t)t + (lane & 1)) >> shift); };
-    // a wave's units into LDS, as operands
-    auto put = [&](const Part<U>& x, int buf) {
-        const uint32_t tile = wave & 1;
-        if (wave < 2) {
-            // lane 16 g + t: dimensions 32 u + 8 g of tokens t and 16 + t
-            const uint32_t g = lane >> 4, at = ((g & 1) * 32 + (lane & 15)) * 16;
+    // their scales: keys' in lanes 0 and 1, values' in 2 and 3
+    auto load_scales = [&](uint32_t found) {
+        return (lane & 2 ? a.v_scale : a.k_scale)[(uint64_t)(found < a.seqs.blocks ? found : 0) * a.heads + h];
+    };
+    // a wave's share of a step's codes: keys or values of one tile, all units of it or half of them
+    const bool keys = !(wave & 2);
+    const uint32_t u0 = wave / 4 * SHARE;
+    auto load_codes = [&](uint32_t found, int t, u32x4 (&w)[SHARE]) {
+        const uint32_t page = of_lane(found, wave & 1);
+        const uint64_t cell = (uint64_t)(page < a.seqs.blocks ? page : 0) * a.heads + h;
+        const uint64_t at = ((cell << shift) + (((uint32_t)t + (wave & 1)) & ((1u << shift) - 1))) * (U * UNIT_BYTES) + u0 * UNIT_BYTES + lane * 16;
+        const uint8_t* codes = keys ? a.k : a.v;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                uint8_t* p = mem.k[buf][tile][2 * u + (g >> 1)] + at;
-                *reinterpret_cast<f16x8*>(p) = operand(x.w[u][0], x.w[u][1]);
-                *reinterpret_cast<f16x8*>(p + 16 * 16) = operand(x.w[u][2], x.w[u][3]);
+        for (int u = 0; u < SHARE; ++u) w[u] = *reinterpret_cast<const u32x4*>(codes + at + u * UNIT_BYTES);
+    };
+    // and into LDS, as operands
+    auto put = [&](const u32x4 (&w)[SHARE], int kb, int vb) {
+        const uint32_t tile = wave & 1, g = lane >> 4;
+        if (keys) {
+            // lane 16 g + t: dimensions 32 u + 8 g of tokens t and 16 + t
+            const uint32_t at = ((g & 1) * 32 + (lane & 15)) * 16;
+#pragma unroll
+            for (int u = 0; u < SHARE; ++u) {
+                uint8_t* p = mem.k[kb][tile][2 * (u0 + u) + (g >> 1)] + at;
+                *reinterpret_cast<f16x8*>(p) = operand(w[u][0], w[u][1]);
+                *reinterpret_cast<f16x8*>(p + 16 * 16) = operand(w[u][2], w[u][3]);
             }
         } else {
             // lane 16 g + d: tokens 4 g, then 16 + 4 g, of dimensions d, then 16 + d
-            const uint32_t g = lane >> 4, at = ((g & 1) * 32 + (lane & 15)) * 16 + (g >> 1) * 8;
+            const uint32_t at = ((g & 1) * 32 + (lane & 15)) * 16 + (g >> 1) * 8;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < SHARE; ++u)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t v[2];
-                        halves(x.w[u][2 * b + m], v);
-                        *reinterpret_cast<u32x2*>(mem.v[buf][tile][u][m] + at + b * 16 * 16) = u32x2{v[0], v[1]};
+                        halves(w[u][2 * b + m], v);
+                        *reinterpret_cast<u32x2*>(mem.v[vb][tile][u0 + u][m] + at + b * 16 * 16) = u32x2{v[0], v[1]};
                     }
         }
     };
-    auto compute = [&](int t, int buf, const Scales& c) {
-        f32x16 s[2];
+    auto scores = [&](f32x16 (&s)[NC], int kb, int tile) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
+            for (int e = 0; e < 16; ++e) s[c][e] = 0.0f;
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) {
-                const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.k[buf][i][u] + lane * 16);
+        for (int u = 0; u < 2 * U; ++u) {
+            const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.k[kb][tile][u] + lane * 16);
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) s[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, q[u][j], s[i], 0, 0, 0);
-            }
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, q[c][u][j], s[c], 0, 0, 0);
         }
+    };
+    // masks, and the running maximum; what takes scores and weights further.  A weight of one part
+    // comes out of the exponential times the values' scale, to 2^-23 of the scale's logarithm;
+    // zeros, signs and what is no number are seen to afterwards.
+    float f[NC], down, up;
+    bool odd;
+    auto begin = [&](f32x16 (&s)[NC], int t, float ks, float vs) {
         const int at = t * (int)TILE_TOKENS;
-        float f[2] = {factor * c.k[0], factor * c.k[1]}, most = -inf();
-        // all rows see all of the tiles' tokens, and the larger product is the larger score; or not
-        if (!(at >= lo_most && at + 2 * (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && c.k[0] >= 0.0f && c.k[1] >= 0.0f)) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) f[c] = factor[c] * ks;
+        // all rows see all of the tile's tokens, and the larger product is the larger score; or not
+        if (!(at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f)) {
             asm volatile("");   // not to be done and then selected from
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int c = 0; c < NC; ++c) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int pos = at + i * (int)TILE_TOKENS + 8 * (e / 4) + 4 * (int)hh + e % 4;
-                    s[i][e] = pos <= hi && pos >= lo ? s[i][e] * f[i] : -inf();
+                    const int pos = at + 8 * (e / 4) + 4 * (int)hh + e % 4;
+                    s[c][e] = pos <= hi[c] && pos >= lo[c] ? s[c][e] * f[c] : -inf();
                 }
-                f[i] = 1.0f;
+                f[c] = 1.0f;
             }
         }
+        const bool number = fabsf(vs) < inf();
+        const float unit = scale_exponent(vs);
+        odd = !(vs > 0.0f) || !number;
+        down = number ? vs * P_DOWN : 0.0f;
+        if constexpr (NP == 1) {
+            const float size = number && vs != 0.0f ? fabsf(vs) : 1.0f;
+            down = __builtin_amdgcn_logf(size) + P_DOWN_LOG2;
+            up = OUT * __builtin_amdgcn_rcpf(size);
+        }
+        float next[NC];
+        bool moved = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int c = 0; c < NC; ++c) {
             float m = -inf();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, s[i][e]);
-            m = max_of_halves(m * f[i]);
-            most = fmaxf(most, m + scale_exponent(c.v[i]));
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, s[c][e]);
+            m = max_of_halves(m * f[c]);
             // values without a number to scale them: no number to the rows that see one of them
-            if (!(fabsf(c.v[i]) < inf()) && m != -inf()) sum = __uint_as_float(0x7fc00000u);
+            if (!number && m != -inf()) sum[c] = __uint_as_float(0x7fc00000u);
+            next[c] = REF_TOP - (m + unit);
+            moved |= next[c] < ref[c] - LAG;
         }
-        const float next = REF_TOP - most;
-        if (__ballot(next < ref - LAG)) {
-            const float down_by = next < ref ? exp2_of(next - ref) : 1.0f;
-            sum *= down_by;
+        if (__ballot(moved)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) acc[u] *= down_by;
-            ref = fminf(ref, next);
-        }
-        const float base = ref == inf() ? 0.0f : ref;
+            for (int c = 0; c < NC; ++c) {
+                const float down_by = next[c] < ref[c] ? exp2_of(next[c] - ref[c]) : 1.0f;
+                sum[c] *= down_by;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float down = fabsf(c.v[i]) < inf() ? c.v[i] * P_DOWN : 0.0f;
-            float part = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                s[i][e] = exp2_of(fmaf(s[i][e], f[i], base));
-                part += s[i][e];
-                s[i][e] *= down;
+                for (int u = 0; u < U; ++u) acc[c][u] *= down_by;
+                ref[c] = fminf(ref[c], next[c]);
             }
-            sum += part;
+        }
+    };
+    auto finish = [&](f32x16 (&s)[NC], int vb, int tile, float vs) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                f16x8 p[NP];
+        for (int m = 0; m < 2; ++m) {
+            f16x8 p[NC][NP];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const float base = (ref[c] == inf() ? 0.0f : ref[c]) + (NP == 1 ? down : 0.0f);
+                float part = 0.0f;
+#pragma unroll
+                for (int e = 8 * m; e < 8 * m + 8; ++e) {
+                    s[c][e] = exp2_of(fmaf(s[c][e], f[c], base));
+                    part += s[c][e];
+                    if (NP > 1) s[c][e] *= down;
+                }
+                sum[c] = NP == 1 ? fmaf(part, up, sum[c]) : sum[c] + part;
 #pragma unroll
                 for (int j = 0; j < NP; ++j)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        p[j][e] = (_Float16)s[i][8 * m + e];
-                        s[i][8 * m + e] -= (float)p[j][e];
+                        p[c][j][e] = (_Float16)s[c][8 * m + e];
+                        s[c][8 * m + e] -= (float)p[c][j][e];
                     }
+            }
+            if (NP == 1 && odd) {
+                asm volatile("");
+                const uint32_t sign = vs < 0.0f ? 0x80008000u : 0u, keep = fabsf(vs) > 0.0f && fabsf(vs) < inf() ? ~0u : 0u;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.v[buf][i][u][m] + lane * 16);
+                for (int c = 0; c < NC; ++c) {
+                    u32x4 w = __builtin_bit_cast(u32x4, p[c][0]);
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, p[j], acc[u], 0, 0, 0);
+                    for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ (sign & keep);
+                    p[c][0] = __builtin_bit_cast(f16x8, w);
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.v[vb][tile][u][m] + lane * 16);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        acc[c][u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, p[c][j], acc[c][u], 0, 0, 0);
             }
         }
     };
 
     if (from < to) {
-        // while a step is worked on, the codes of the next one are turned into operands, those of
-        // the one after it loaded, and its successor's blocks looked up; past the last step the same again
+        // Of each tile, its scores' products are issued among the exponentials of the one before,
+        // whose own products with the values follow.  A step is two tiles: the next step's codes go
+        // into LDS in its first half, those after them are asked for, blocks are looked up one
+        // more ahead.  Past the last step the same again.
         auto next_of = [&](int t) { return t + 2 < to ? t + 2 : t; };
-        Part<U> x;
-        Scales now, then;
         int t1 = next_of(from), t2 = next_of(t1);
-        x.load(a, pages(from), from, shift, h, wave, lane);
-        uint32_t found = pages(t1);
-        put(x, 0);
-        now.set(a, x);
-        x.load(a, found, t1, shift, h, wave, lane);
-        found = pages(t2);
-        int buf = 0;
+        uint32_t found = pages(from), found1 = pages(t1);
+        u32x4 w[SHARE];
+        load_codes(found, from, w);
+        float scales = load_scales(found);
+        put(w, 0, 0);
+        load_codes(found1, t1, w);
+        float scales1 = load_scales(found1);
+        uint32_t found2 = pages(t2);
         __syncthreads();
+        f32x16 s0[NC], s1[NC];
+        scores(s0, 0, 0);
+        int kb = 0, vb = 0;
+        const float none = __uint_as_float(0x7fc00000u);
         for (int t = from; t < to; t += 2) {
-            put(x, buf ^ 1);
-            then.set(a, x);
-            x.load(a, found, t2, shift, h, wave, lane);
+            const float ks0 = of_lane(found, 0) < a.seqs.blocks ? of_lane(scales, 0) : none, vs0 = of_lane(scales, 2);
+            const float ks1 = of_lane(found, 1) < a.seqs.blocks ? of_lane(scales, 1) : none, vs1 = of_lane(scales, 3);
+            const int vn = vb == 2 ? 0 : vb + 1;
+            begin(s0, t, ks0, vs0);
+            scores(s1, kb, 1);
+            finish(s0, vb, 0, vs0);
+            put(w, kb ^ 1, vn);
+            load_codes(found2, t2, w);
+            found = found1;
+            scales = scales1;
+            scales1 = load_scales(found2);
+            found1 = found2;
             t2 = next_of(t2);
-            found = pages(t2);
-            compute(t, buf, now);
-            now = then;
-            buf ^= 1;
+            found2 = pages(t2);
             __syncthreads();
+            begin(s1, t + 1, ks1, vs1);
+            kb ^= 1;
+            scores(s0, kb, 0);
+            finish(s1, vb, 1, vs1);
+            vb = vn;
         }
+        __syncthreads();
     }
 
-    sum += __shfl_xor(sum, 32);
-    if (k.parts > 1) {
-        if (!real) return;
-        float* ws = form_of<ROWS>(a).ws + ((uint64_t)k.slot * ROWS + 32 * wave + r) * (32 * U + 4);
-        if (hh == 0) {
-            ws[0] = ref;
-            ws[1] = sum;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4*>(ws + 4 + 32 * u + 8 * j + 4 * hh) =
-                    f32x4{acc[u][4 * j], acc[u][4 * j + 1], acc[u][4 * j + 2], acc[u][4 * j + 3]};
-        return;
-    }
-    // through LDS, so that rows leave whole
     typedef T four __attribute__((ext_vector_type(4)));
-    const float up = sum == 0.0f ? 0.0f : OUT / sum;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int c = 0; c < NC; ++c) {
+        const uint32_t i = 32 * (WAVES * c + wave) + r;
+        sum[c] += __shfl_xor(sum[c], 32);
+        if (k.parts > 1) {
+            float* ws = form_of<ROWS>(a).ws + ((uint64_t)k.slot * ROWS + i) * (32 * U + 4);
+            if (i >= k.have) continue;
+            if (hh == 0) {
+                ws[0] = ref[c];
+                ws[1] = sum[c];
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<four*>(&mem.rows[32 * wave + r][32 * u + 8 * j + 4 * hh]) =
-                four{(T)(acc[u][4 * j] * up), (T)(acc[u][4 * j + 1] * up), (T)(acc[u][4 * j + 2] * up), (T)(acc[u][4 * j + 3] * up)};
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4*>(ws + 4 + 32 * u + 8 * j + 4 * hh) =
+                        f32x4{acc[c][u][4 * j], acc[c][u][4 * j + 1], acc[c][u][4 * j + 2], acc[c][u][4 * j + 3]};
+        } else {   // through LDS, so that rows leave whole
+            const float up = sum[c] == 0.0f ? 0.0f : OUT / sum[c];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<four*>(&mem.rows[i][32 * u + 8 * j + 4 * hh]) =
+                        four{(T)(acc[c][u][4 * j] * up), (T)(acc[c][u][4 * j + 1] * up), (T)(acc[c][u][4 * j + 2] * up),
+                             (T)(acc[c][u][4 * j + 3] * up)};
+        }
+    }
+    if (k.parts > 1) return;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < k.have * (8 * U); i += blockDim.x) {
         const uint32_t row = i / (8 * U), d = i % (8 * U) * 4;

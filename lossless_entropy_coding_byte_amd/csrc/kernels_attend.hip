@@ -10,9 +10,9 @@ namespace {
 constexpr int WAVES = 4;
 constexpr int THREADS = 64 * WAVES;
 
-// Rows of 256 dimensions of 24 bits do not fit the registers of the form for many.
+// Rows of 192 dimensions of 24 bits do not fit the registers of the form for many.
 template <typename T, int U>
-constexpr bool HAS_MANY = sizeof(T) == 2 || U < 8;
+constexpr bool HAS_MANY = sizeof(T) == 2 || U < 6;
 
 // A workgroup takes one item.  Those of the first launch without one see to the
 // rows of no sequence.
@@ -28,11 +28,11 @@ __global__ __launch_bounds__(THREADS, U * sizeof(T) <= 16 ? 2 : 1) void attend_f
 }
 
 template <typename T, int U>
-__global__ __launch_bounds__(THREADS, U <= 4 && U * sizeof(T) < 16 ? 2 : 1) void attend_many_kernel(AttendArgs a) {
+__global__ __launch_bounds__((2 * MANY_ROWS<T, U>), U * sizeof(T) <= 8 ? 2 : 1) void attend_many_kernel(AttendArgs a) {
     __shared__ __attribute__((aligned(16))) ManyMemory<T, U> memory;
     const uint32_t h = blockIdx.x % a.heads, w = blockIdx.x / a.heads;
     Item it;
-    if (find_item<MANY_ROWS, false>(a, w, threadIdx.x & 63, it))
+    if (find_item<MANY_ROWS<T, U>, false>(a, w, threadIdx.x & 63, it))
         attend_many<T, U>(a, it, h, memory);
     else if (a.fill)
         fill_rows<T>(a, (w - it.slot) * a.heads + h, (gridDim.x / a.heads - it.slot) * a.heads);
@@ -110,8 +110,8 @@ __global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a, uint
     if (blockIdx.x < few_items) {
         if (find_item<FEW_ROWS, true>(a, blockIdx.x, lane, it))
             join<T, U, FEW_ROWS, true>(a, it, blockIdx.y, blockIdx.z, gridDim.z, memory);
-    } else if (MANY && find_item<MANY_ROWS, true>(a, blockIdx.x - few_items, lane, it)) {
-        join<T, U, MANY_ROWS, false>(a, it, blockIdx.y, blockIdx.z, gridDim.z, memory);
+    } else if (MANY && find_item<MANY_ROWS<T, U>, true>(a, blockIdx.x - few_items, lane, it)) {
+        join<T, U, MANY_ROWS<T, U>, false>(a, it, blockIdx.y, blockIdx.z, gridDim.z, memory);
     }
 }
 
@@ -125,11 +125,12 @@ struct Shape {
     uint64_t slots;          // of all heads
     uint32_t target, shortest;
 };
-Shape shape_of(bool many, uint32_t dim, uint32_t heads, uint32_t group, uint32_t block, uint64_t seqs, uint64_t tokens, uint64_t width,
+// rows: of a workgroup.
+Shape shape_of(uint64_t rows, uint32_t dim, uint32_t heads, uint32_t group, uint32_t block, uint64_t seqs, uint64_t tokens, uint64_t width,
                uint64_t few) {
-    const uint64_t rows = many ? MANY_ROWS : FEW_ROWS;
+    const bool many = rows != FEW_ROWS;
     Shape s;
-    s.target = (uint32_t)((many ? 2 : 4) * device_cu_count());
+    s.target = (uint32_t)((many ? rows == 128 ? 2 : 1 : 4) * device_cu_count());
     s.shortest = many ? 16 : dim <= 128 ? 4 : 8;
     // a sequence's rows, rounded up; none has more than `few` in the form for few
     uint64_t most = tokens * group / rows + seqs;
@@ -145,14 +146,14 @@ Shape shape_of(bool many, uint32_t dim, uint32_t heads, uint32_t group, uint32_t
     if (!split) s.shortest = 0x7ffffffeu;
     return s;
 }
-uint64_t bytes_of(const Shape& s, bool many, uint32_t dim) {
-    return s.slots * (many ? MANY_ROWS : FEW_ROWS) * (padded_dim(dim) + 4) * sizeof(float);
+uint64_t bytes_of(const Shape& s, uint64_t rows, uint32_t dim) {
+    return s.slots * rows * (padded_dim(dim) + 4) * sizeof(float);
 }
 
 // Rows of a sequence up to which the form for few takes it: 64, or all where a call
 // has too few in all to be worth a second form's launch.
 uint32_t few_most(int type, uint32_t dim, uint64_t rows) {
-    return (type == LECB_F32 && dim > 192) || rows <= 256 ? 0x7fffffffu : 64;
+    return (type == LECB_F32 && dim > 128) || rows <= 256 ? 0x7fffffffu : 64;
 }
 
 template <typename F>
@@ -172,7 +173,7 @@ int launch(AttendArgs a, const Shape* shape, bool few, bool many, hipStream_t st
     if constexpr (HAS_MANY<T, U>)
         if (many) {
             hipLaunchKernelGGL(HIP_KERNEL_NAME(attend_many_kernel<T, U>), dim3((uint32_t)(shape[1].items * a.heads)),
-                               dim3(THREADS), 0, st, a);
+                               dim3(2 * MANY_ROWS<T, U>), 0, st, a);
             joins[1] = (uint32_t)shape[1].joins;
             a.fill = 0;
         }
@@ -202,11 +203,12 @@ int launch(AttendArgs a, const Shape* shape, bool few, bool many, hipStream_t st
 uint64_t attention_q8_workspace(const lecb_cache_q8& c, uint64_t seqs, uint64_t tokens, uint64_t width, uint32_t heads) {
     // for every type, and with starts or without
     const uint32_t group = heads / c.heads;
-    uint64_t bytes = 0;
-    for (int many = 0; many < 2; ++many)
-        bytes += bytes_of(shape_of(many, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group)),
-                          many, c.dim);
-    return bytes;
+    auto bytes = [&](uint64_t rows) {
+        return bytes_of(shape_of(rows, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group)),
+                        rows, c.dim);
+    };
+    const uint64_t many = bytes(128), more = bytes(256);
+    return bytes(FEW_ROWS) + (many > more ? many : more);
 }
 
 int launch_attention_q8(const AttentionQ8& x, void* stream) {
@@ -218,17 +220,18 @@ int launch_attention_q8(const AttentionQ8& x, void* stream) {
                     static_cast<const uint8_t*>(x.cache.v), x.cache.k_scale, x.cache.v_scale, x.q_token, x.q_head, x.out_token,
                     x.out_head, x.cache.heads, group, x.cache.dim, x.window, x.causal, x.fill,
                     x.scale * 1.44269504088896340736f, most, {}};
-    Shape shape[2];
-    float* ws = static_cast<float*>(x.ws);
-    for (int i = 0; i < 2; ++i) {
-        shape[i] = shape_of(i, a.dim, a.heads, group, x.cache.block, x.seqs.seqs, x.seqs.tokens, x.seqs.width, most);
-        a.form[i] = {ws, shape[i].target, shape[i].shortest, (uint32_t)shape[i].slots};
-        ws += bytes_of(shape[i], i, x.cache.dim) / sizeof(float);
-    }
     return with_float_type(x.type, [&](auto t) {
         typedef decltype(t) T;
         return with_units(x.cache.dim, [&](auto units) {
             constexpr int U = decltype(units)::value;
+            constexpr uint64_t ROWS[2] = {FEW_ROWS, MANY_ROWS<T, U>};
+            Shape shape[2];
+            float* ws = static_cast<float*>(x.ws);
+            for (int i = 0; i < 2; ++i) {
+                shape[i] = shape_of(ROWS[i], a.dim, a.heads, group, x.cache.block, x.seqs.seqs, x.seqs.tokens, x.seqs.width, most);
+                a.form[i] = {ws, shape[i].target, shape[i].shortest, (uint32_t)shape[i].slots};
+                ws += bytes_of(shape[i], ROWS[i], a.dim) / sizeof(float);
+            }
             return launch<T, U>(a, shape, few, many, static_cast<hipStream_t>(stream));
         });
     });
