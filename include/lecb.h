@@ -670,7 +670,7 @@ typedef struct {
     const int32_t* lengths;   /* [seqs] */
     const int32_t* starts;    /* [seqs + 1] or NULL (then tokens = seqs) */
     uint64_t table_stride;
-    uint32_t width;           /* width * block below 2^31 */
+    uint32_t width;           /* width * block below 2^30 */
     uint32_t seqs;            /* below 2^20 */
     uint32_t tokens;          /* below 2^27 */
 } lecb_cache_seqs;

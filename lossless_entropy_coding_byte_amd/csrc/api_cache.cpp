@@ -22,7 +22,7 @@ bool cache_ok(const lecb_cache_q8* c) {
 // OK, or the error
 int seqs_status(const lecb_cache_q8& c, const lecb_cache_seqs* s) {
     if (!s) return LECB_ERR_INVALID_ARG;
-    if (s->seqs >= (1u << 20) || s->tokens >= (1u << 27) || (uint64_t)s->width * c.block >= (1ull << 31))
+    if (s->seqs >= (1u << 20) || s->tokens >= (1u << 27) || (uint64_t)s->width * c.block >= (1ull << 30))
         return LECB_ERR_TOO_LARGE;
     if (s->tokens == 0) return LECB_OK;
     if (!s->starts && s->tokens != s->seqs) return LECB_ERR_INVALID_ARG;
@@ -65,7 +65,7 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
 uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t seqs, uint32_t tokens, uint32_t width,
                                            uint32_t heads) {
     if (!cache || !geometry_ok(*cache) || heads < 1 || heads % cache->heads || seqs >= (1u << 20) ||
-        tokens >= (1u << 27) || (uint64_t)width * cache->block >= (1ull << 31) || !seqs || !tokens)
+        tokens >= (1u << 27) || (uint64_t)width * cache->block >= (1ull << 30) || !seqs || !tokens)
         return 0;
     return attention_q8_workspace(*cache, seqs, tokens, width, heads);
 }

@@ -266,9 +266,9 @@ constexpr float OUT = 0x1p19f;       // and back
 constexpr int SCALE_LOW = -60;
 
 __device__ inline float scale_exponent(float s) {
-    // infinities and NaN give 0, and so does zero: all that counts is that p stays finite
+    // infinities and NaN give 0, as all that counts is that p stays finite; zero the lowest, to stand behind all others
     const int e = __builtin_amdgcn_frexp_expf(s);
-    return (float)(e > SCALE_LOW ? e : SCALE_LOW);
+    return (float)(s == 0.0f ? SCALE_LOW : e > SCALE_LOW ? e : SCALE_LOW);
 }
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // The largest of the lanes 32 apart, and of those 16 apart.

@@ -6,25 +6,25 @@
 #if defined(__HIPCC__)
 namespace lecb {
 
-// Few rows: a workgroup takes 16 NT rows of one head over a part of the tiles,
+// Few rows: a workgroup takes 16 rows of one head over a part of the tiles,
 // its waves tile by tile in turn, each with a softmax of its own; their sums are
 // joined at the end.  Matrix instructions by 16 x 16 x 32, transposed: codes of
 // 16 tokens (then of 16 dimensions of the values) times the rows, so that a row's
 // scores stand in one lane of each 16, four tokens each, and are the second
 // product's operand as they are; values are stored in that order of tokens.
 // Neither codes nor scores go through LDS.
-template <typename T, int U, int NT, int WAVES>
+template <typename T, int U, int WAVES>
 struct FewMemory {
     union {
-        T q[16 * NT][32 * U];
-        float sum[WAVES][16 * NT][68];
+        T q[FEW_ROWS][32 * U];
+        float sum[WAVES][FEW_ROWS][68];
     };
-    float ref[WAVES][16 * NT], l[WAVES][16 * NT];
+    float ref[WAVES][FEW_ROWS], l[WAVES][FEW_ROWS];
 };
 
-template <typename T, int U, int NT, int WAVES>
-__device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<T, U, NT, WAVES>& mem) {
-    constexpr int ROWS = 16 * NT, NQ = Parts<T>::Q, NP = Parts<T>::P, THREADS = 64 * WAVES;
+template <typename T, int U, int WAVES>
+__device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<T, U, WAVES>& mem) {
+    constexpr int ROWS = FEW_ROWS, NQ = Parts<T>::Q, NP = Parts<T>::P, THREADS = 64 * WAVES;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     Work k;
     if (!work_of<ROWS>(a, it, h, k)) return;
@@ -70,28 +70,17 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
     stage_rows(a, k, h, ROWS, 32 * U, &mem.q[0][0]);
     __syncthreads();
 
-    // rows: lane r of each 16 has row r of each 16, dimensions 32 u + 8 g and on
-    f16x8 q[NT][U][NQ];
-    float factor[NT];
-    int hi[NT], lo[NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const uint32_t row = k.r0 + 16 * c + r;
-        factor[c] = load_row<T, U, 16>(a, mem.q[16 * c + r], 8 * g, 32, q[c]);
-        const int at = k.old + (row < k.rows ? (int)(row / a.group) : 0);
-        hi[c] = a.causal ? at : k.len - 1;
-        lo[c] = a.window ? at - (int)a.window + 1 : 0;
-    }
+    // rows: lane r of each 16 has row r, dimensions 32 u + 8 g and on
+    const uint32_t row = k.r0 + r;
+    f16x8 q[U][NQ];
+    const float factor = load_row<T, U, 16>(a, mem.q[r], 8 * g, 32, q);
+    const int pos = k.old + (row < k.rows ? (int)(row / a.group) : 0);
+    const int hi = a.causal ? pos : k.len - 1, lo = a.window ? pos - (int)a.window + 1 : 0;
 
-    f32x4 acc[NT][2 * U];
-    float ref[NT], sum[NT];
+    f32x4 acc[2 * U];
+    float ref = inf(), sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        ref[c] = inf();
-        sum[c] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2 * U; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int i = 0; i < 2 * U; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     // Codes have one set of registers: the next tile's keys are asked for once this one's are
     // operands, its values after theirs, its block one tile ahead.  Past the last tile the
@@ -99,19 +88,14 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
     for (; t < to; t += WAVES) {
         const int t1 = next_of(t), at = t * (int)TILE_TOKENS;
         const float ks = none ? __uint_as_float(0x7fc00000u) : of_lane(scales, 0), vs = of_lane(scales, 1);
-        f32x4 s[NT][2];
-#pragma unroll
-        for (int c = 0; c < NT; ++c) s[c][0] = s[c][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const f16x8 codes = operand(kc[u][2 * b], kc[u][2 * b + 1]);
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j)
-                        s[c][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, q[c][u][j], s[c][b], 0, 0, 0);
+                for (int j = 0; j < NQ; ++j) s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, q[u][j], s[b], 0, 0, 0);
             }
         const uint64_t cell = cell_of(found), next_at = place(cell, t1);
         load_codes(a.k, next_at, kc);
@@ -123,93 +107,79 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         const bool plain = at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f;
         const bool number = fabsf(vs) < inf();
         const float down = number ? vs * P_DOWN : 0.0f, unit = scale_exponent(vs);
-        f16x8 p[NT][NP];
+        float f = factor * ks, v[8], most = -inf();
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            float f = factor[c] * ks, v[8], most = -inf();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = s[c][i / 4][i % 4];
-            if (!plain) {
-                asm volatile("");   // not to be done and then selected from
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int pos = at + 4 * (int)g + i % 4 + i / 4 * 16;
-                    v[i] = pos <= hi[c] && pos >= lo[c] ? v[i] * f : -inf();
-                }
-                f = 1.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) most = fmaxf(most, v[i]);
-            most = max_of_quarters(most * f);
-            // values without a number to scale them: no number to the rows that see one of them
-            if (!number && most != -inf()) sum[c] = __uint_as_float(0x7fc00000u);
-            const float next = REF_TOP - (most + unit);
-            if (__ballot(next < ref[c] - LAG)) {
-                const float down_by = next < ref[c] ? exp2_of(next - ref[c]) : 1.0f;
-                sum[c] *= down_by;
-#pragma unroll
-                for (int i = 0; i < 2 * U; ++i) acc[c][i] *= down_by;
-                ref[c] = fminf(ref[c], next);
-            }
-            const float base = ref[c] == inf() ? 0.0f : ref[c];
+        for (int i = 0; i < 8; ++i) v[i] = s[i / 4][i % 4];
+        if (!plain) {
+            asm volatile("");   // not to be done and then selected from
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[i] = exp2_of(fmaf(v[i], f, base));
-                sum[c] += v[i];
-                v[i] *= down;
+                const int token = at + 4 * (int)g + i % 4 + i / 4 * 16;
+                v[i] = token <= hi && token >= lo ? v[i] * f : -inf();
             }
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[c][j][i] = (_Float16)v[i];
-                    v[i] -= (float)p[c][j][i];
-                }
+            f = 1.0f;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, v[i]);
+        most = max_of_quarters(most * f);
+        // values without a number to scale them: no number to the rows that see one of them
+        if (!number && most != -inf()) sum = __uint_as_float(0x7fc00000u);
+        const float next = REF_TOP - (most + unit);
+        if (__ballot(next < ref - LAG)) {
+            const float down_by = next < ref ? exp2_of(next - ref) : 1.0f;
+            sum *= down_by;
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i) acc[i] *= down_by;
+            ref = fminf(ref, next);
+        }
+        const float base = ref == inf() ? 0.0f : ref;
+        f16x8 p[NP];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = exp2_of(fmaf(v[i], f, base));
+            sum += v[i];
+            v[i] *= down;
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[j][i] = (_Float16)v[i];
+                v[i] -= (float)p[j][i];
+            }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const f16x8 codes = operand(vc[u][2 * b], vc[u][2 * b + 1]);
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int j = 0; j < NP; ++j)
-                        acc[c][2 * u + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, p[c][j], acc[c][2 * u + b], 0, 0, 0);
+                for (int j = 0; j < NP; ++j)
+                    acc[2 * u + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, p[j], acc[2 * u + b], 0, 0, 0);
             }
         load_codes(a.v, next_at, vc);
     }
     __syncthreads();   // the rows in LDS are no longer needed
 
     // the waves' sums, joined in their order
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        sum[c] += __shfl_xor(sum[c], 16);
-        sum[c] += __shfl_xor(sum[c], 32);
-        if (g == 0) {
-            mem.ref[wave][16 * c + r] = ref[c];
-            mem.l[wave][16 * c + r] = sum[c];
-        }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (g == 0) {
+        mem.ref[wave][r] = ref;
+        mem.l[wave][r] = sum;
     }
     __syncthreads();
+    float lowest = mem.ref[0][r];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        float least = mem.ref[0][16 * c + r];
+    for (int i = 1; i < WAVES; ++i) lowest = fminf(lowest, mem.ref[i][r]);
+    const float down_by = ref == lowest ? 1.0f : exp2_of(lowest - ref);
 #pragma unroll
-        for (int i = 1; i < WAVES; ++i) least = fminf(least, mem.ref[i][16 * c + r]);
-        const float down_by = ref[c] == least ? 1.0f : exp2_of(least - ref[c]);
-#pragma unroll
-        for (int i = 0; i < 2 * U; ++i) acc[c][i] *= down_by;
-    }
+    for (int i = 0; i < 2 * U; ++i) acc[i] *= down_by;
     float* ws = form_of<ROWS>(a).ws + (uint64_t)k.slot * ROWS * (32 * U + 4);
 #pragma unroll
     for (int d0 = 0; d0 < U; d0 += 2) {
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (2 * d0 + i < 2 * U)
-                    *reinterpret_cast<f32x4*>(&mem.sum[wave][16 * c + r][16 * i + 4 * g]) = acc[c][2 * d0 + i];
+        for (int i = 0; i < 4; ++i)
+            if (2 * d0 + i < 2 * U) *reinterpret_cast<f32x4*>(&mem.sum[wave][r][16 * i + 4 * g]) = acc[2 * d0 + i];
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < ROWS * 16; i += THREADS) {
             const uint32_t row = i / 16, d = i % 16 * 4, at = 32 * d0 + d;

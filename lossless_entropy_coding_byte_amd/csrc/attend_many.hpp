@@ -32,7 +32,7 @@ struct ManyMemory {
 
 template <typename T, int U>
 __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t h, ManyMemory<T, U>& mem) {
-    constexpr int WAVES = MANY_WAVES<T, U>, ROWS = MANY_ROWS<T, U>, SHARE = 4 * U / WAVES, NC = 1, NQ = Parts<T>::Q, NP = Parts<T>::P;
+    constexpr int WAVES = MANY_WAVES<T, U>, ROWS = MANY_ROWS<T, U>, SHARE = 4 * U / WAVES, NQ = Parts<T>::Q, NP = Parts<T>::P;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, hh = lane >> 5;
     Work k;
     if (!work_of<ROWS>(a, it, h, k)) return;
@@ -42,36 +42,25 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     }
     const uint32_t seq = it.seq;
 
-    // rows: lane r of each 32 has row r of each of the wave's 32, dimensions 16 e + 8 hh and on
+    // rows: lane r of each 32 has row r of the wave's, dimensions 16 e + 8 hh and on
     stage_rows(a, k, h, ROWS, 32 * U, &mem.rows[0][0]);
     __syncthreads();
-    f16x8 q[NC][2 * U][NQ];
-    float factor[NC];
-    int hi[NC], lo[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const uint32_t i = 32 * (WAVES * c + wave) + r, row = k.r0 + i;
-        factor[c] = load_row<T, 2 * U, 32>(a, mem.rows[i], 8 * hh, 16, q[c]);
-        const int at = k.old + (row < k.rows ? (int)(row / a.group) : 0);
-        hi[c] = a.causal ? at : k.len - 1;
-        lo[c] = a.window ? at - (int)a.window + 1 : 0;
-    }
+    const uint32_t mine = 32 * wave + r, row = k.r0 + mine;
+    f16x8 q[2 * U][NQ];
+    const float factor = load_row<T, 2 * U, 32>(a, mem.rows[mine], 8 * hh, 16, q);
+    const int pos = k.old + (row < k.rows ? (int)(row / a.group) : 0);
+    const int hi = a.causal ? pos : k.len - 1, lo = a.window ? pos - (int)a.window + 1 : 0;
     __syncthreads();
     // tiles go by pairs: what a pair has too many is masked
     const int from = k.from, to = k.to, lo_most = k.lo_most, hi_least = k.hi_least;
     const uint32_t shift = __builtin_ctz(a.seqs.block / TILE_TOKENS);
 
-    f32x16 acc[NC][U];
-    float ref[NC], sum[NC];
+    f32x16 acc[U];
+    float ref = inf(), sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        ref[c] = inf();
-        sum[c] = 0.0f;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c][u][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
 
     // the blocks of a step's tiles t and t + 1, in even and odd lanes
     auto pages = [&](int t) { return a.seqs.page(seq, ((uint32_t)t + (lane & 1)) >> shift); };
@@ -117,44 +106,35 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
                     }
         }
     };
-    auto scores = [&](f32x16 (&s)[NC], int kb, int tile) {
+    auto scores = [&](f32x16& s, int kb, int tile) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[c][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 2 * U; ++u) {
             const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.k[kb][tile][u] + lane * 16);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) s[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, q[c][u][j], s[c], 0, 0, 0);
+            for (int j = 0; j < NQ; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, q[u][j], s, 0, 0, 0);
         }
     };
     // masks, and the running maximum; what takes scores and weights further.  A weight of one part
     // comes out of the exponential times the values' scale, to 2^-23 of the scale's logarithm;
     // zeros, signs and what is no number are seen to afterwards.
-    float f[NC], down, up;
+    float f, down, up;
     bool odd;
-    auto begin = [&](f32x16 (&s)[NC], int t, float ks, float vs) {
+    auto begin = [&](f32x16& s, int t, float ks, float vs) {
         const int at = t * (int)TILE_TOKENS;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) f[c] = factor[c] * ks;
+        f = factor * ks;
         // all rows see all of the tile's tokens, and the larger product is the larger score; or not
         if (!(at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f)) {
             asm volatile("");   // not to be done and then selected from
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int pos = at + 8 * (e / 4) + 4 * (int)hh + e % 4;
-                    s[c][e] = pos <= hi[c] && pos >= lo[c] ? s[c][e] * f[c] : -inf();
-                }
-                f[c] = 1.0f;
+            for (int e = 0; e < 16; ++e) {
+                const int token = at + 8 * (e / 4) + 4 * (int)hh + e % 4;
+                s[e] = token <= hi && token >= lo ? s[e] * f : -inf();
             }
+            f = 1.0f;
         }
         const bool number = fabsf(vs) < inf();
-        const float unit = scale_exponent(vs);
         odd = !(vs > 0.0f) || !number;
         down = number ? vs * P_DOWN : 0.0f;
         if constexpr (NP == 1) {
@@ -162,72 +142,54 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
             down = __builtin_amdgcn_logf(size) + P_DOWN_LOG2;
             up = OUT * __builtin_amdgcn_rcpf(size);
         }
-        float next[NC];
-        bool moved = false;
+        float m = -inf();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float m = -inf();
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, s[e]);
+        m = max_of_halves(m * f);
+        // values without a number to scale them: no number to the rows that see one of them
+        if (!number && m != -inf()) sum = __uint_as_float(0x7fc00000u);
+        const float next = REF_TOP - (m + scale_exponent(vs));
+        if (__ballot(next < ref - LAG)) {
+            const float down_by = next < ref ? exp2_of(next - ref) : 1.0f;
+            sum *= down_by;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, s[c][e]);
-            m = max_of_halves(m * f[c]);
-            // values without a number to scale them: no number to the rows that see one of them
-            if (!number && m != -inf()) sum[c] = __uint_as_float(0x7fc00000u);
-            next[c] = REF_TOP - (m + unit);
-            moved |= next[c] < ref[c] - LAG;
-        }
-        if (__ballot(moved)) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const float down_by = next[c] < ref[c] ? exp2_of(next[c] - ref[c]) : 1.0f;
-                sum[c] *= down_by;
-#pragma unroll
-                for (int u = 0; u < U; ++u) acc[c][u] *= down_by;
-                ref[c] = fminf(ref[c], next[c]);
-            }
+            for (int u = 0; u < U; ++u) acc[u] *= down_by;
+            ref = fminf(ref, next);
         }
     };
-    auto finish = [&](f32x16 (&s)[NC], int vb, int tile, float vs) {
+    auto finish = [&](f32x16& s, int vb, int tile, float vs) {
+        const float base = (ref == inf() ? 0.0f : ref) + (NP == 1 ? down : 0.0f);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            f16x8 p[NC][NP];
+            f16x8 p[NP];
+            float part = 0.0f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const float base = (ref[c] == inf() ? 0.0f : ref[c]) + (NP == 1 ? down : 0.0f);
-                float part = 0.0f;
-#pragma unroll
-                for (int e = 8 * m; e < 8 * m + 8; ++e) {
-                    s[c][e] = exp2_of(fmaf(s[c][e], f[c], base));
-                    part += s[c][e];
-                    if (NP > 1) s[c][e] *= down;
-                }
-                sum[c] = NP == 1 ? fmaf(part, up, sum[c]) : sum[c] + part;
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[c][j][e] = (_Float16)s[c][8 * m + e];
-                        s[c][8 * m + e] -= (float)p[c][j][e];
-                    }
+            for (int e = 8 * m; e < 8 * m + 8; ++e) {
+                s[e] = exp2_of(fmaf(s[e], f, base));
+                part += s[e];
+                if (NP > 1) s[e] *= down;
             }
+            sum = NP == 1 ? fmaf(part, up, sum) : sum + part;
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[j][e] = (_Float16)s[8 * m + e];
+                    s[8 * m + e] -= (float)p[j][e];
+                }
             if (NP == 1 && odd) {
                 asm volatile("");
-                const uint32_t sign = vs < 0.0f ? 0x80008000u : 0u, keep = fabsf(vs) > 0.0f && fabsf(vs) < inf() ? ~0u : 0u;
+                const uint32_t keep = fabsf(vs) > 0.0f && fabsf(vs) < inf() ? ~0u : 0u, sign = vs < 0.0f ? 0x80008000u & keep : 0u;
+                u32x4 w = __builtin_bit_cast(u32x4, p[0]);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    u32x4 w = __builtin_bit_cast(u32x4, p[c][0]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ (sign & keep);
-                    p[c][0] = __builtin_bit_cast(f16x8, w);
-                }
+                for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ sign;
+                p[0] = __builtin_bit_cast(f16x8, w);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const f16x8 codes = *reinterpret_cast<const f16x8*>(mem.v[vb][tile][u][m] + lane * 16);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int j = 0; j < NP; ++j)
-                        acc[c][u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, p[c][j], acc[c][u], 0, 0, 0);
+                for (int j = 0; j < NP; ++j) acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes, p[j], acc[u], 0, 0, 0);
             }
         }
     };
@@ -248,7 +210,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         float scales1 = load_scales(found1);
         uint32_t found2 = pages(t2);
         __syncthreads();
-        f32x16 s0[NC], s1[NC];
+        f32x16 s0, s1;
         scores(s0, 0, 0);
         int kb = 0, vb = 0;
         const float none = __uint_as_float(0x7fc00000u);
@@ -277,36 +239,32 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         __syncthreads();
     }
 
-    typedef T four __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const uint32_t i = 32 * (WAVES * c + wave) + r;
-        sum[c] += __shfl_xor(sum[c], 32);
-        if (k.parts > 1) {
-            float* ws = form_of<ROWS>(a).ws + ((uint64_t)k.slot * ROWS + i) * (32 * U + 4);
-            if (i >= k.have) continue;
-            if (hh == 0) {
-                ws[0] = ref[c];
-                ws[1] = sum[c];
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<f32x4*>(ws + 4 + 32 * u + 8 * j + 4 * hh) =
-                        f32x4{acc[c][u][4 * j], acc[c][u][4 * j + 1], acc[c][u][4 * j + 2], acc[c][u][4 * j + 3]};
-        } else {   // through LDS, so that rows leave whole
-            const float up = sum[c] == 0.0f ? 0.0f : OUT / sum[c];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<four*>(&mem.rows[i][32 * u + 8 * j + 4 * hh]) =
-                        four{(T)(acc[c][u][4 * j] * up), (T)(acc[c][u][4 * j + 1] * up), (T)(acc[c][u][4 * j + 2] * up),
-                             (T)(acc[c][u][4 * j + 3] * up)};
+    sum += __shfl_xor(sum, 32);
+    if (k.parts > 1) {
+        if (mine >= k.have) return;
+        float* ws = form_of<ROWS>(a).ws + ((uint64_t)k.slot * ROWS + mine) * (32 * U + 4);
+        if (hh == 0) {
+            ws[0] = ref;
+            ws[1] = sum;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4*>(ws + 4 + 32 * u + 8 * j + 4 * hh) =
+                    f32x4{acc[u][4 * j], acc[u][4 * j + 1], acc[u][4 * j + 2], acc[u][4 * j + 3]};
+        return;
     }
-    if (k.parts > 1) return;
+    // through LDS, so that rows leave whole
+    typedef T four __attribute__((ext_vector_type(4)));
+    const float over = sum == 0.0f ? 0.0f : OUT / sum;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<four*>(&mem.rows[mine][32 * u + 8 * j + 4 * hh]) =
+                four{(T)(acc[u][4 * j] * over), (T)(acc[u][4 * j + 1] * over), (T)(acc[u][4 * j + 2] * over),
+                     (T)(acc[u][4 * j + 3] * over)};
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < k.have * (8 * U); i += blockDim.x) {
         const uint32_t row = i / (8 * U), d = i % (8 * U) * 4;

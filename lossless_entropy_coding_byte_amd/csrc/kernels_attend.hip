@@ -7,6 +7,7 @@ namespace lecb {
 
 namespace {
 
+constexpr uint32_t FAR = 1u << 30;   // no row of the table holds more tokens
 constexpr int WAVES = 4;
 constexpr int THREADS = 64 * WAVES;
 
@@ -18,11 +19,11 @@ constexpr bool HAS_MANY = sizeof(T) == 2 || U < 6;
 // rows of no sequence.
 template <typename T, int U>
 __global__ __launch_bounds__(THREADS, U * sizeof(T) <= 16 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
-    __shared__ __attribute__((aligned(16))) FewMemory<T, U, 1, WAVES> memory;
+    __shared__ __attribute__((aligned(16))) FewMemory<T, U, WAVES> memory;
     const uint32_t h = blockIdx.x % a.heads, w = blockIdx.x / a.heads;
     Item it;
     if (find_item<FEW_ROWS, false>(a, w, threadIdx.x & 63, it))
-        attend_few<T, U, 1, WAVES>(a, it, h, memory);
+        attend_few<T, U, WAVES>(a, it, h, memory);
     else if (a.fill)
         fill_rows<T>(a, (w - it.slot) * a.heads + h, (gridDim.x / a.heads - it.slot) * a.heads);
 }
@@ -150,10 +151,15 @@ uint64_t bytes_of(const Shape& s, uint64_t rows, uint32_t dim) {
     return s.slots * rows * (padded_dim(dim) + 4) * sizeof(float);
 }
 
-// Rows of a sequence up to which the form for few takes it: 64, or all where a call
-// has too few in all to be worth a second form's launch.
-uint32_t few_most(int type, uint32_t dim, uint64_t rows) {
-    return (type == LECB_F32 && dim > 128) || rows <= 256 ? 0x7fffffffu : 64;
+// Rows of a sequence up to which the form for few takes it.  Both forms, us, heads
+// of 128 dimensions in bf16: 16 sequences of 8192 tokens with 64 rows each 124 and 149,
+// one of 32768 48 and 52, 16 of 1024 33 and 39; with 128 rows 65 and 55 (32768), 34
+// and 43 (1024), with 512 181 and 98, 98 and 65; dimensions of 64 and 256 and 32 bits cross
+// between 64 and 256 rows too.  Each form takes a launch, 4 to 5 us where it finds nothing to
+// do: a call of few rows in all goes by the form for few alone, one sequence by one of them.
+uint32_t few_most(int type, uint32_t dim, uint64_t rows, uint64_t seqs) {
+    if ((type == LECB_F32 && dim > 128) || rows <= (seqs > 1 ? 256 : 64)) return 0x7fffffffu;
+    return seqs > 1 ? 64 : 0;
 }
 
 template <typename F>
@@ -204,7 +210,7 @@ uint64_t attention_q8_workspace(const lecb_cache_q8& c, uint64_t seqs, uint64_t 
     // for every type, and with starts or without
     const uint32_t group = heads / c.heads;
     auto bytes = [&](uint64_t rows) {
-        return bytes_of(shape_of(rows, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group)),
+        return bytes_of(shape_of(rows, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group, seqs)),
                         rows, c.dim);
     };
     const uint64_t many = bytes(128), more = bytes(256);
@@ -214,11 +220,11 @@ uint64_t attention_q8_workspace(const lecb_cache_q8& c, uint64_t seqs, uint64_t 
 int launch_attention_q8(const AttentionQ8& x, void* stream) {
     const uint32_t group = x.heads / x.cache.heads;
     const uint64_t rows = (uint64_t)x.seqs.tokens * group, longest = x.seqs.starts ? rows : group;   // a sequence may have all of them
-    const uint32_t most = few_most(x.type, x.cache.dim, rows);
-    const bool many = longest > most, few = !many || x.seqs.starts;
+    const uint32_t most = few_most(x.type, x.cache.dim, rows, x.seqs.seqs);
+    const bool many = longest > most, few = most > 0 && (!many || x.seqs.starts);
     AttendArgs a = {seqs_of(x.cache, x.seqs), x.q, x.out, static_cast<const uint8_t*>(x.cache.k),
                     static_cast<const uint8_t*>(x.cache.v), x.cache.k_scale, x.cache.v_scale, x.q_token, x.q_head, x.out_token,
-                    x.out_head, x.cache.heads, group, x.cache.dim, x.window, x.causal, x.fill,
+                    x.out_head, x.cache.heads, group, x.cache.dim, x.window < FAR ? x.window : FAR, x.causal, x.fill,
                     x.scale * 1.44269504088896340736f, most, {}};
     return with_float_type(x.type, [&](auto t) {
         typedef decltype(t) T;

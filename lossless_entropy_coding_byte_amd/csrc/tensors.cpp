@@ -463,8 +463,8 @@ struct Sequences {
         } else if (tokens != seqs) {
             refuse(name + ": without starts there is one row for each sequence");
         }
-        if (seqs >= 1 << 20 || tokens >= 1 << 27 || table.size(1) * cache.c.block >= int64_t(1) << 31)
-            refuse(name + ": fewer than 2^20 sequences, 2^27 rows and 2^31 tokens to a row of the table");
+        if (seqs >= 1 << 20 || tokens >= 1 << 27 || table.size(1) * cache.c.block >= int64_t(1) << 30)
+            refuse(name + ": fewer than 2^20 sequences, 2^27 rows and 2^30 tokens to a row of the table");
         s = {static_cast<int32_t*>(ptr(table)), static_cast<int32_t*>(ptr(lengths)), static_cast<int32_t*>(ptr(starts)),
              (uint64_t)(seqs > 1 ? table.stride(0) : table.size(1)), (uint32_t)table.size(1), (uint32_t)seqs, (uint32_t)tokens};
     }

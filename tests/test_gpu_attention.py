@@ -78,6 +78,35 @@ def test_prompt_of_one_sequence(dtype):
     check(gen(1), [700], [700], 3, 1, 128, 64, dtype)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 72, 128, 160, 256])
+def test_prompts_that_see_all_tokens(dim, dtype):
+    """Many rows without a causal mask, and with windows of one token and of more than there are."""
+    check(gen(dim), [150, 333, 2], [150, 90, 2], 4, 2, dim, 64, dtype, causal=False)
+    check(gen(dim), [150, 333, 2], [150, 90, 2], 4, 2, dim, 64, dtype, window=1)
+    check(gen(dim), [150, 333, 2], [150, 90, 2], 4, 2, dim, 64, dtype, window=(1 << 31) - 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news", [[3, 1], [120, 60]])
+def test_scales_of_either_sign_and_zeros(news, dtype):
+    """A code stands for code * scale, whatever the scale's sign; blocks of zeros stand beside blocks of small numbers."""
+    g = gen(32)
+    cache = random_cache(g, 12, 2, 64, 32, DEV)
+    for s in (cache.k_scale, cache.v_scale):
+        s.mul_(torch.where(torch.rand(12, 2, generator=g) < 0.4, -1.0, 1.0).to(DEV))
+    table, lens = tables(g, [150, 200], 32, 12, DEV)
+    starts = starts_of(news, DEV)
+    q = queries(g, sum(news), 4, 64, dtype)
+    for scale in (None, -0.1):
+        want, tol = attention(q, cache, table, lens, starts, scale=scale)
+        near(lecb.attention_q8(q, cache, table, lens, starts, scale=scale), want, tol)
+    cache.v_scale.copy_(torch.where(torch.rand(12, 2, generator=g) < 0.4, 0.0, 2.0**-50))
+    if dtype != F16:
+        want, tol = attention(q, cache, table, lens, starts)
+        near(lecb.attention_q8(q, cache, table, lens, starts), want, tol)
+
+
 def test_many_sequences():
     check(gen(3), [(s * 41) % 130 for s in range(200)], None, 2, 1, 64, 32, BF16)
 
@@ -181,6 +210,27 @@ def test_what_is_masked_never_matters():
         assert torch.equal(lecb.attention_q8(q, cache, poisoned, lens, starts, window=20), want)
         # rows of one call that see different blocks: the first row of three ends where the third's block begins
         cache.k.copy_(codes), cache.v.copy_(values)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompts_past_blocks_without_a_number(dtype):
+    """Many rows: those from the bad block on are NaN, for keys, values and the table; windows pass it by again."""
+    g = gen(15)
+    for bad, field in ((math.nan, "k_scale"), (math.nan, "v_scale"), (math.inf, "v_scale"), (None, "table")):
+        cache = random_cache(g, 20, 1, 64, 32, DEV)
+        table, lens = tables(g, [600], 32, 20, DEV)
+        starts = starts_of([600], DEV)
+        q = queries(g, 600, 2, 64, dtype)
+        want, tol = attention(q, cache, table, lens, starts, window=64)
+        if field == "table":
+            table[0, 5] = -1
+        else:
+            getattr(cache, field)[table[0, 5].item()] = bad
+        got = lecb.attention_q8(q, cache, table, lens, starts, window=64)
+        away = torch.ones(600, dtype=torch.bool)
+        away[160 : 192 + 63] = False
+        near(got[away.to(DEV)], want[away], tol[away])
+        assert bool(got[160 : 192 + 63].isnan().all())
 
 
 def test_rows_that_see_no_number_are_nan_and_no_others():
