@@ -270,6 +270,13 @@ __device__ inline float scale_exponent(float s) {
     const int e = __builtin_amdgcn_frexp_expf(s);
     return (float)(s == 0.0f ? SCALE_LOW : e > SCALE_LOW ? e : SCALE_LOW);
 }
+// a * b rounded to 32 bits before it is split: the compiler would fuse the product with the
+// first part's conversion, which now and then rounds the other way than what the second part is the rest of.
+__device__ inline float product(float a, float b) {
+    float p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // The largest of the lanes 32 apart, and of those 16 apart.
 __device__ inline float max_of_halves(float v) {

@@ -138,7 +138,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         for (int i = 0; i < 8; ++i) {
             v[i] = exp2_of(fmaf(v[i], f, base));
             sum += v[i];
-            v[i] *= down;
+            v[i] = NP > 1 ? product(v[i], down) : v[i] * down;
         }
 #pragma unroll
         for (int j = 0; j < NP; ++j)

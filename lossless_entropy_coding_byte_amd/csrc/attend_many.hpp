@@ -167,7 +167,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
             for (int e = 8 * m; e < 8 * m + 8; ++e) {
                 s[e] = exp2_of(fmaf(s[e], f, base));
                 part += s[e];
-                if (NP > 1) s[e] *= down;
+                if (NP > 1) s[e] = product(s[e], down);
             }
             sum = NP == 1 ? fmaf(part, up, sum) : sum + part;
 #pragma unroll

@@ -126,6 +126,12 @@ def test_queries_of_every_size(dtype, size):
     check(gen(6), [100, 37], [2, 1], 4, 2, 64, 32, dtype, size=size, scale=1 / size)
 
 
+@pytest.mark.parametrize("lengths,news,window", [([9] * 300, None, None), ([300], [300], 9)])
+def test_weights_in_two_parts(lengths, news, window):
+    """Results of 32 bits: the weights' two parts belong together, in each of some 170000 weights of about a ninth."""
+    check(gen(34), lengths, news, 64, 1, 4, 32, F32, size=0.3, window=window)
+
+
 def test_queries_with_small_and_large_elements():
     """A row's elements down to 2^-29 of its largest are exact, and what meets codes of 0 adds nothing."""
     g = gen(7)
