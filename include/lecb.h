@@ -716,18 +716,20 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  * (> 0, causal = 1 only) over the last `window` of these.  A row that sees
  * nothing is 0.  q and out: type F32, BF16 or F16, element (row, head, i) at row *
  * token stride + head * head stride + i; out must not overlap q.
- * Codes are exact in the products, q to 2^-30 of its row's largest element, sums
- * and the softmax have 32 bits; its weights enter the second product with 11
- * bits (BF16 out) or 22.  Scales of values are told apart from 2^-60 up.
- * A row with an infinity or NaN in q is NaN, and so is one that sees a
- * block whose scale is NaN, a block that is not one of the cache's, or whose sequence's
- * length exceeds width * block.  What a row does not see never matters.  Rows
+ * Codes are exact in the products, q to 2^-29 of its row's largest element (F16:
+ * exact), sums and the softmax have 32 bits; its weights enter the second product
+ * with 11 bits (BF16 out) or 22, down to 2^-36 of the largest of weight times scale.
+ * Values whose scales are below 2^-60 lose as many of these 36 bits as they are below it.
+ * A row with an infinity or NaN in q is NaN, and so is one that sees a block
+ * whose scale of values is not finite or whose scale of keys is NaN, a block that is not one of the
+ * cache's, or whose sequence's length exceeds width * block.  What a row does not see never matters.  Rows
  * of no sequence: as in lecb_cache_read_q8.
- * How the work is split, and with it the order of sums, depends on the lengths
- * of all sequences; the same call gives the same bits.
+ * How the work is split, and with it the order of sums and a result's last places,
+ * depends on the lengths of all sequences; the same call gives the same bits.
  * d_ws: lecb_attention_q8_workspace_bytes (may be 0, then NULL is taken); its
  * contents do not matter before or after.
- * Errors: INVALID_ARG, WORKSPACE, TOO_LARGE (also tokens * heads >= 2^31). */
+ * heads is a multiple of the cache's.  Errors: INVALID_ARG (window >= 2^31 too), WORKSPACE,
+ * TOO_LARGE (also tokens * heads >= 2^27, seqs * cache heads >= 2^22). */
 uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t seqs, uint32_t tokens,
                                            uint32_t width, uint32_t heads);
 int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_stride, int type, uint32_t heads,

@@ -14,6 +14,16 @@ namespace lecb {
 // rows: a row's scores stand in two lanes, which is the second product's operand,
 // with tokens 16 m + 8 (i / 4) + 4 (lane / 32) + i % 4 as its eight, so the
 // values' operands are put together in that order.
+//
+// Bound by instruction issue: of a tile and 32 rows, 512 cycles of products stand
+// beside some 600 of vector instructions, a third of them exponentials and a
+// fifth (a tenth with eight waves) codes to halves.  512 tokens after 32256, 32 heads to 8 of 128
+// dimensions: 298 us, 915 TFLOP/s, the matrix units busy 42 % of the time (four waves
+// and two workgroups a compute unit 323); two prompts of up to 4096 tokens 265, 690.  Dimensions of 96
+// have three units, which eight waves do not share evenly; more than 128, or 32 bits, need
+// the registers of two waves.  Tried and slower: 64 rows a wave (half the reads of LDS, but one
+// wave a SIMD, and sums outside of the vector registers: 340 -> 399 us), all products of a step
+// in one go after its softmax (332 -> 364).
 template <typename T, int U>
 constexpr int MANY_WAVES = U <= 4 && U != 3 && sizeof(T) == 2 ? 8 : 4;
 template <typename T, int U>

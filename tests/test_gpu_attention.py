@@ -312,6 +312,22 @@ def test_rows_of_no_sequence():
         assert bool((out[:3] == 7).all()) and bool((out[8:] == 7).all()) and torch.equal(out[3:8], got[3:8])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 144, 256])
+def test_one_sequence(dim, dtype):
+    """One sequence goes by one of the forms: many heads to one, no starts; few rows of its own before many of none."""
+    g = gen(36)
+    check(g, [300], None, 100, 1, dim, 64, dtype)
+    check(g, [3000], None, 100, 1, dim, 64, dtype)
+    for length in (300, 3000):
+        cache = random_cache(g, 50, 1, dim, 64, DEV)
+        table, lens = tables(g, [length], 64, 50, DEV)
+        starts = torch.tensor([2, 7], dtype=torch.int32, device=DEV)
+        q = queries(g, 90, 2, dim, dtype)
+        want, tol = attention(q, cache, table, lens, starts)
+        near(lecb.attention_q8(q, cache, table, lens, starts), want, tol)
+
+
 def test_strides():
     """Queries and results as columns of wider buffers, at odd addresses, heads before tokens."""
     g = gen(20)
