@@ -106,10 +106,10 @@ def main(argv=None):
         y, h = step(x, r, norm_weight, up, down)
     for _ in range(3):
         x.copy_(randn(*x.shape))
-        r.copy_(h)
         graph.replay()
         want, _ = step(x, r, norm_weight, up, down)
         assert torch.equal(y, want), "a replay gives what the eager step gives"
+        r.copy_(h)   # behind a replay: the capture itself has written nothing
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     start.record()
     for _ in range(50):
