@@ -278,6 +278,9 @@ __device__ inline float product(float a, float b) {
     return p;
 }
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+// What takes sums of weights to a reference that is d (<= 0) away, as the root of it: multiplied in twice.  References lie
+// up to 2^188 apart where the scales do, further than one factor reaches, and sums of weights up to 2^94 each still count then.
+__device__ inline float root_of(float d) { return exp2_of(0.5f * d); }
 // The largest of the lanes 32 apart, and of those 16 apart.
 __device__ inline float max_of_halves(float v) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

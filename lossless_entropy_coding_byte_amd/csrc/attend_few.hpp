@@ -134,8 +134,8 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         if (!number && most != -inf()) sum = __uint_as_float(0x7fc00000u);
         const float next = REF_TOP - (most + unit);
         if (__ballot(next < ref - LAG)) {
-            const float down_by = next < ref ? exp2_of(next - ref) : 1.0f;
-            sum *= down_by;
+            const float root = next < ref ? root_of(next - ref) : 1.0f, down_by = root * root;
+            sum = sum * root * root;
 #pragma unroll
             for (int i = 0; i < 2 * U; ++i) acc[i] *= down_by;
             ref = fminf(ref, next);
@@ -199,7 +199,10 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
 #pragma unroll
             for (int j = 1; j < WAVES; ++j) least = fminf(least, mem.ref[j][row]);
 #pragma unroll
-            for (int j = 0; j < WAVES; ++j) l += mem.l[j][row] * (mem.ref[j][row] == least ? 1.0f : exp2_of(least - mem.ref[j][row]));
+            for (int j = 0; j < WAVES; ++j) {
+                const float root = mem.ref[j][row] == least ? 1.0f : root_of(least - mem.ref[j][row]);
+                l += mem.l[j][row] * root * root;
+            }
             if (k.parts > 1) {
                 *reinterpret_cast<f32x4*>(ws + row * (32 * U + 4) + 4 + at) = v;
                 if (at == 0) {

@@ -160,8 +160,8 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         if (!number && m != -inf()) sum = __uint_as_float(0x7fc00000u);
         const float next = REF_TOP - (m + scale_exponent(vs));
         if (__ballot(next < ref - LAG)) {
-            const float down_by = next < ref ? exp2_of(next - ref) : 1.0f;
-            sum *= down_by;
+            const float root = next < ref ? root_of(next - ref) : 1.0f, down_by = root * root;
+            sum = sum * root * root;
 #pragma unroll
             for (int u = 0; u < U; ++u) acc[u] *= down_by;
             ref = fminf(ref, next);

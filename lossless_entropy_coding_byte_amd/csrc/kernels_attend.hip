@@ -60,9 +60,9 @@ __device__ inline void join(const AttendArgs& a, const Item& it, uint32_t h, uin
                 const float* w = ws + p * step;
                 const float r = w[0], next = fminf(ref, r), l2 = w[1];
                 const f32x4 x = *reinterpret_cast<const f32x4*>(w + 4 + d);
-                const float was = ref == next ? 1.0f : exp2_of(next - ref), is = r == next ? 1.0f : exp2_of(next - r);
-                v = v * was + x * is;
-                l = l * was + l2 * is;
+                const float was = ref == next ? 1.0f : root_of(next - ref), is = r == next ? 1.0f : root_of(next - r);
+                v = v * (was * was) + x * (is * is);
+                l = l * was * was + l2 * is * is;
                 ref = next;
             }
         }
@@ -86,9 +86,9 @@ __device__ inline void join(const AttendArgs& a, const Item& it, uint32_t h, uin
                 l = 0.0f;
 #pragma unroll
                 for (int j = 0; j < SHARES; ++j) {
-                    const float f = s_ref[j] == least ? 1.0f : exp2_of(least - s_ref[j]);
-                    v += *reinterpret_cast<const f32x4*>(s_sum + j * 32 * U + d) * f;
-                    l += s_l[j] * f;
+                    const float root = s_ref[j] == least ? 1.0f : root_of(least - s_ref[j]);
+                    v += *reinterpret_cast<const f32x4*>(s_sum + j * 32 * U + d) * (root * root);
+                    l += s_l[j] * root * root;
                 }
             }
             __syncthreads();
