@@ -127,10 +127,13 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         }
     };
     // masks, and the running maximum; what takes scores and weights further.  A weight of one part
-    // comes out of the exponential times the values' scale, to 2^-23 of the scale's logarithm;
-    // zeros, signs and what is no number are seen to afterwards.
-    float f, down, up;
-    bool odd;
+    // comes out of the exponential times the values' scale, to 2^-23 of the scale's logarithm, and its
+    // sum takes the scale off again.  That holds where the scale is a number that the reciprocal
+    // reaches and no more than 2^60 below the largest so far (the exponential's range then leaves 77 bits
+    // below equal weights of that block); other scales, of either sign and zero, are multiplied in after the sum.
+    float f, lift = 0.0f, up = 1.0f;
+    bool odd = false;
+    uint32_t high = 0;   // the bits of the largest scale so far
     auto begin = [&](f32x16& s, int t, float ks, float vs) {
         const int at = t * (int)TILE_TOKENS;
         f = factor * ks;
@@ -145,12 +148,13 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
             f = 1.0f;
         }
         const bool number = fabsf(vs) < inf();
-        odd = !(vs > 0.0f) || !number;
-        down = number ? vs * P_DOWN : 0.0f;
         if constexpr (NP == 1) {
-            const float size = number && vs != 0.0f ? fabsf(vs) : 1.0f;
-            down = __builtin_amdgcn_logf(size) + P_DOWN_LOG2;
-            up = OUT * __builtin_amdgcn_rcpf(size);
+            // in scalar registers: 2^-60 to 2^100, and 2^60 over the bits' exponent
+            const uint32_t bits = __float_as_uint(vs), size = bits & 0x7fffffffu;
+            if (size < 0x7f800000u && size > high) high = size;
+            odd = bits - 0x21800000u > 0x71800000u - 0x21800000u || size + (60u << 23) < high;
+            lift = odd ? 0.0f : __builtin_amdgcn_logf(vs) + P_DOWN_LOG2;
+            up = odd ? 1.0f : OUT * __builtin_amdgcn_rcpf(vs);
         }
         float m = -inf();
 #pragma unroll
@@ -168,7 +172,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         }
     };
     auto finish = [&](f32x16& s, int vb, int tile, float vs) {
-        const float base = (ref == inf() ? 0.0f : ref) + (NP == 1 ? down : 0.0f);
+        const float base = (ref == inf() ? 0.0f : ref) + lift;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             f16x8 p[NP];
@@ -177,7 +181,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
             for (int e = 8 * m; e < 8 * m + 8; ++e) {
                 s[e] = exp2_of(fmaf(s[e], f, base));
                 part += s[e];
-                if (NP > 1) s[e] = product(s[e], down);
+                if (NP > 1) s[e] = product(s[e], fabsf(vs) < inf() ? vs * P_DOWN : 0.0f);
             }
             sum = NP == 1 ? fmaf(part, up, sum) : sum + part;
 #pragma unroll
@@ -185,15 +189,13 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     p[j][e] = (_Float16)s[8 * m + e];
-                    s[8 * m + e] -= (float)p[j][e];
+                    if (NP > 1) s[8 * m + e] -= (float)p[j][e];
                 }
             if (NP == 1 && odd) {
-                asm volatile("");
-                const uint32_t keep = fabsf(vs) > 0.0f && fabsf(vs) < inf() ? ~0u : 0u, sign = vs < 0.0f ? 0x80008000u & keep : 0u;
-                u32x4 w = __builtin_bit_cast(u32x4, p[0]);
+                asm volatile("");   // not to be done and then selected from
+                const float down = fabsf(vs) < inf() ? vs * P_DOWN : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ sign;
-                p[0] = __builtin_bit_cast(f16x8, w);
+                for (int e = 0; e < 8; ++e) p[0][e] = (_Float16)(s[8 * m + e] * down);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {

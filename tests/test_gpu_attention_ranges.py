@@ -11,6 +11,7 @@ from test_gpu_layers import DEV, gen
 
 pytestmark = pytest.mark.gpu
 TYPES = [BF16, F16, F32]
+SMALL = [2.0**-60, 2.0**-99, 2.0**-100, 2.0**-108, 2.0**-109, 2.0**-110, 2.0**-126, 2.0**-127, 2.0**-149]
 
 
 def lost(tokens):
@@ -42,3 +43,67 @@ def check_far_apart(low, high, dtype, length, rows):
                                                (F32, 5000, 40)])
 def test_scales_far_apart(dtype, length, rows, low, high):
     check_far_apart(low, high, dtype, length, rows)
+
+
+@pytest.mark.parametrize("low,high", FAR)
+@pytest.mark.parametrize("length,rows", [(300, 200), (5000, 300)])
+def test_scales_far_apart_for_many_rows(length, rows, low, high):
+    check_far_apart(low, high, BF16, length, rows)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_a_block_of_tiny_values_among_others(dim, dtype):
+    """Many rows: those that see the block get what the others give, those before it and past its window do not change."""
+    g = gen(dim)
+    cache = random_cache(g, 22, 1, dim, 32, DEV)
+    table, lens = tables(g, [320, 200], 32, 22, DEV)
+    news = [300, 120]
+    starts = starts_of(news, DEV)
+    q = queries(g, sum(news), 2, dim, dtype)
+    block, ordinary = table[0, 5].item(), cache.v_scale.clone()      # tokens 160 .. 191: rows 140 .. 171
+    for window in (None, 64):
+        away = torch.ones(sum(news), dtype=torch.bool, device=DEV)
+        away[140 : 300 if window is None else 172 + 63] = False
+        plain = lecb.attention_q8(q, cache, table, lens, starts, window=window)
+        for scale in SMALL:
+            for sign in (1, -1):
+                cache.v_scale[block] = sign * scale
+                got = lecb.attention_q8(q, cache, table, lens, starts, window=window)
+                assert torch.equal(got[away], plain[away])
+            want, tol = attention(q, cache, table, lens, starts, window=window)
+            near(got, want, tol + lost(320))
+        cache.v_scale.copy_(ordinary)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("field", ["k_scale", "v_scale"])
+def test_a_block_kept_for_tokens_to_come(field, dtype):
+    """The block behind a sequence's last, an odd one, whose scales nobody has written: the same bits whatever they hold."""
+    g = gen(7)
+    cache = random_cache(g, 12, 2, 128, 32, DEV)
+    table, lens = tables(g, [288], 32, 12, DEV, width=10)
+    table[0, 9] = next(b for b in range(12) if b not in table[0].tolist())
+    starts = starts_of([288], DEV)
+    q = queries(g, 288, 4, 128, dtype)
+    want = lecb.attention_q8(q, cache, table, lens, starts)
+    for scale in SMALL + [0.0, 3e38, float("inf"), float("nan")]:
+        getattr(cache, field)[table[0, 9].item()] = scale
+        assert torch.equal(lecb.attention_q8(q, cache, table, lens, starts), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", SMALL)
+def test_both_forms_on_the_same_rows(scale, dtype):
+    """Rows of a prompt, and each of them alone, over blocks of tiny values and of ordinary ones."""
+    g = gen(9)
+    cache = random_cache(g, 10, 1, 64, 32, DEV)
+    table, lens = tables(g, [300], 32, 10, DEV)
+    cache.v_scale[table[0, ::3].long()] = scale
+    q = queries(g, 300, 1, 64, dtype)
+    want, tol = attention(q, cache, table, lens, starts_of([300], DEV))
+    near(lecb.attention_q8(q, cache, table, lens, starts_of([300], DEV)), want, tol + lost(300))
+    rows = torch.arange(0, 300, 7)
+    each = (rows + 1).to(torch.int32).to(DEV)
+    got = lecb.attention_q8(q[rows.to(DEV)], cache, table.repeat(len(rows), 1), each)
+    near(got, want[rows], tol[rows] + lost(300))
