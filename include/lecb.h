@@ -721,7 +721,7 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  * with 11 bits (BF16 out) or 22, down to 2^-36 of the largest of weight times scale.
  * Values whose scales are below 2^-60 lose as many of these 36 bits as they are below it.
  * A row with an infinity or NaN in q is NaN, and so is one that sees a block
- * whose scale of values is not finite or whose scale of keys is NaN, a block that is not one of the
+ * with a scale that is not finite, a block that is not one of the
  * cache's, or whose sequence's length exceeds width * block.  What a row does not see never matters.  Rows
  * of no sequence: as in lecb_cache_read_q8.
  * How the work is split, and with it the order of sums and a result's last places,

@@ -143,7 +143,7 @@ def attention_q8(q, cache: CacheQ8, table, lengths, starts=None, scale: float | 
     heads is a multiple of the cache's: query head h reads head h // (heads / cache heads).  A row sees its
     sequence's tokens up to its own (causal: all of them where false), the last ``window`` of these if given.
     scale: 1 / sqrt(dim).  Returns [tokens, heads, dim] in q's type.  A row that sees nothing is 0; so is a row of
-    no sequence, which a given ``out`` keeps as it was.  A row that sees a block with a scale of NaN, one
+    no sequence, which a given ``out`` keeps as it was.  A row that sees a block with a scale that is not finite, one
     that is not the cache's, or that belongs to a sequence longer than its row of the table, is NaN; what
     is masked never matters.  The order of sums follows from the lengths of all sequences.  out: must not
     overlap what is read.  ws: a uint8 workspace of lecb_attention_q8_workspace_bytes that the caller keeps; calls

@@ -292,6 +292,12 @@ __device__ inline float max_of_quarters(float v) {
 }
 __device__ inline float inf() { return __uint_as_float(0x7f800000u); }
 
+// A block's scale of keys; NaN where it is no number or there is no such block: an infinite one would leave tokens
+// whose products are negative out of the softmax, which their keys, infinities and 0 times infinity, are not.
+__device__ inline float key_scale(float s, bool there) {
+    return there && (__float_as_uint(s) & 0x7fffffffu) < 0x7f800000u ? s : __uint_as_float(0x7fc00000u);
+}
+
 // Rows of q into LDS, `pitch` elements apart, zeros past the head's dimensions and
 // past the last row: what all waves of a workgroup then take their operands from.
 template <typename T>

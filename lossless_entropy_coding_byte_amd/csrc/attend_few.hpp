@@ -95,7 +95,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
     // same one is loaded again.
     for (; t < to; t += WAVES) {
         const int t1 = next_of(t), at = t * (int)TILE_TOKENS;
-        const float ks = none ? __uint_as_float(0x7fc00000u) : of_lane(scales, 0), vs = of_lane(scales, 1);
+        const float ks = key_scale(of_lane(scales, 0), !none), vs = of_lane(scales, 1);
         f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int u = 0; u < U; ++u)

@@ -225,10 +225,10 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
         f32x16 s0, s1;
         scores(s0, 0, 0);
         int kb = 0, vb = 0;
-        const float none = __uint_as_float(0x7fc00000u);
         for (int t = from; t < to; t += 2) {
-            const float ks0 = of_lane(found, 0) < a.seqs.blocks ? of_lane(scales, 0) : none, vs0 = of_lane(scales, 2);
-            const float ks1 = of_lane(found, 1) < a.seqs.blocks ? of_lane(scales, 1) : none, vs1 = of_lane(scales, 3);
+            const float keys_scales = key_scale(scales, found < a.seqs.blocks);
+            const float ks0 = of_lane(keys_scales, 0), vs0 = of_lane(scales, 2);
+            const float ks1 = of_lane(keys_scales, 1), vs1 = of_lane(scales, 3);
             const int vn = vb == 2 ? 0 : vb + 1;
             begin(s0, t, ks0, vs0);
             scores(s1, kb, 1);

@@ -107,3 +107,26 @@ def test_both_forms_on_the_same_rows(scale, dtype):
     each = (rows + 1).to(torch.int32).to(DEV)
     got = lecb.attention_q8(q[rows.to(DEV)], cache, table.repeat(len(rows), 1), each)
     near(got, want[rows], tol[rows] + lost(300))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news", [7, 200])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_block_whose_keys_are_no_numbers(bad, news, dtype):
+    """Rows that see it are NaN, whatever the sign of their products with its codes; others are what they are."""
+    g = gen(13)
+    cache = random_cache(g, 10, 1, 64, 32, DEV)
+    table, lens = tables(g, [300], 32, 10, DEV)
+    keys = cache.k.cpu()
+    keys[table[0, 9].item()] = keys[table[0, 9].item()].abs()      # tokens 288 .. 299, the last twelve rows
+    cache.k.copy_(keys)
+    starts = starts_of([news], DEV)
+    for sign in (1, -1):
+        q = sign * queries(g, news, 2, 64, dtype).abs()
+        cache.k_scale[table[0, 9].item()] = 0.03
+        want, tol = attention(q, cache, table, lens, starts)
+        cache.k_scale[table[0, 9].item()] = bad
+        got = lecb.attention_q8(q, cache, table, lens, starts)
+        sees = min(news, 12)
+        assert bool(got[news - sees :].isnan().all())
+        near(got[: news - sees], want[: news - sees], tol[: news - sees])
