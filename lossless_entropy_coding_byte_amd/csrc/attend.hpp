@@ -325,10 +325,17 @@ __device__ inline void stage_rows(const AttendArgs& a, const Work& k, uint32_t h
     }
 }
 
+// What takes a row's products of codes to scores, with the block's scale: its power of two, to 2^-163, comes in two halves,
+// so that small queries and large keys, or the other way round, meet within the range of 32 bits and lose nothing.
+struct Factor {
+    float a, b;
+    __device__ float times(float scale) const { return a * scale * b; }
+};
+
 // One row as operands: N pieces of eight dimensions, d0 + step i and on; the lanes
-// that share a row are LANES apart.  Returns what takes a product of codes to a score.
+// that share a row are LANES apart.
 template <typename T, int N, int LANES>
-__device__ inline float load_row(const AttendArgs& a, const T* row, uint32_t d0, uint32_t step, f16x8 (&q)[N][Parts<T>::Q]) {
+__device__ inline Factor load_row(const AttendArgs& a, const T* row, uint32_t d0, uint32_t step, f16x8 (&q)[N][Parts<T>::Q]) {
     typedef T piece __attribute__((ext_vector_type(8)));
     uint32_t top = 0;
 #pragma unroll
@@ -360,7 +367,8 @@ __device__ inline float load_row(const AttendArgs& a, const T* row, uint32_t d0,
             }
         }
     }
-    return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : ldexpf(a.scale, -lift);
+    const int half = lift / 2;
+    return {top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : ldexpf(a.scale, -half), ldexpf(1.0f, half - lift)};
 }
 
 // Four neighbouring results, as far as the head's dimensions go.

@@ -81,7 +81,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
     // rows: lane r of each 16 has row r, dimensions 32 u + 8 g and on
     const uint32_t row = k.r0 + r;
     f16x8 q[U][NQ];
-    const float factor = load_row<T, U, 16>(a, mem.q[r], 8 * g, 32, q);
+    const Factor factor = load_row<T, U, 16>(a, mem.q[r], 8 * g, 32, q);
     const int pos = k.old + (row < k.rows ? (int)(row / a.group) : 0);
     const int hi = a.causal ? pos : k.len - 1, lo = a.window ? pos - (int)a.window + 1 : 0;
 
@@ -115,7 +115,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         const bool plain = at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f;
         const bool number = fabsf(vs) < inf();
         const float down = number ? vs * P_DOWN : 0.0f, unit = scale_exponent(vs);
-        float f = factor * ks, v[8], most = -inf();
+        float f = factor.times(ks), v[8], most = -inf();
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = s[i / 4][i % 4];
         if (!plain) {

@@ -57,7 +57,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     __syncthreads();
     const uint32_t mine = 32 * wave + r, row = k.r0 + mine;
     f16x8 q[2 * U][NQ];
-    const float factor = load_row<T, 2 * U, 32>(a, mem.rows[mine], 8 * hh, 16, q);
+    const Factor factor = load_row<T, 2 * U, 32>(a, mem.rows[mine], 8 * hh, 16, q);
     const int pos = k.old + (row < k.rows ? (int)(row / a.group) : 0);
     const int hi = a.causal ? pos : k.len - 1, lo = a.window ? pos - (int)a.window + 1 : 0;
     __syncthreads();
@@ -136,7 +136,7 @@ __device__ inline void attend_many(const AttendArgs& a, const Item& it, uint32_t
     uint32_t high = 0;   // the bits of the largest scale so far
     auto begin = [&](f32x16& s, int t, float ks, float vs) {
         const int at = t * (int)TILE_TOKENS;
-        f = factor * ks;
+        f = factor.times(ks);
         // all rows see all of the tile's tokens, and the larger product is the larger score; or not
         if (!(at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f)) {
             asm volatile("");   // not to be done and then selected from

@@ -130,3 +130,21 @@ def test_a_block_whose_keys_are_no_numbers(bad, news, dtype):
         sees = min(news, 12)
         assert bool(got[news - sees :].isnan().all())
         near(got[: news - sees], want[: news - sees], tol[: news - sees])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [3, 200])
+@pytest.mark.parametrize("size", [2.0**-133, 2.0**-126, 2.0**-120, 2.0**-112, 2.0**-60, 2.0**100, 2.0**120])
+def test_queries_and_keys_of_opposite_size(size, news, dtype):
+    """Scores of ordinary size out of queries near either end of the range and keys near the other."""
+    g = gen(17)
+    cache = random_cache(g, 10, 1, 64, 32, DEV)
+    cache.k_scale.mul_(min(2.0**120, 0.25 / size))
+    table, lens = tables(g, [300], 32, 10, DEV)
+    starts = starts_of([news], DEV)
+    q = (size * torch.randn(news, 2, 64, generator=g).double()).to(dtype).to(DEV)
+    for scale in (None, 2.0**-40):
+        if scale is not None:
+            cache.k_scale.mul_(2.0**30 if size > 1 else 1.0)
+        want, tol = attention(q, cache, table, lens, starts, scale=scale)
+        near(lecb.attention_q8(q, cache, table, lens, starts, scale=scale), want, tol)
