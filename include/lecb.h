@@ -713,7 +713,7 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  *   out[i][h] = sum_j p_j v_j,  p = softmax_j(scale * q[i][h] . k_j),
  * k_j and v_j of head h / (heads / cache heads), over the sequence's tokens j
  * up to the row's own (causal = 1) or all of them (causal = 0); with a window
- * (> 0, causal = 1 only) over the last `window` of these.  A row that sees
+ * (> 0, causal = 1 only) over the last `window` of these.  scale * log2(e) is finite.  A row that sees
  * nothing is 0.  q and out: type F32, BF16 or F16, element (row, head, i) at row *
  * token stride + head * head stride + i; out must not overlap q.
  * Codes are exact in the products, q to 2^-29 of its row's largest element (F16:

@@ -74,7 +74,7 @@ int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_
                       const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, float scale, int causal,
                       uint32_t window, void* d_out, uint64_t out_token_stride, uint64_t out_head_stride, int fill,
                       void* d_ws, uint64_t ws_bytes, void* stream) {
-    if (!cache_ok(cache) || !float_type(type) || heads < 1 || heads % cache->heads || !std::isfinite(scale) ||
+    if (!cache_ok(cache) || !float_type(type) || heads < 1 || heads % cache->heads || !std::isfinite(scale * LOG2_E) ||
         (causal != 0 && causal != 1) || (fill != 0 && fill != 1) || (window && !causal) || window >= (1u << 31))
         return LECB_ERR_INVALID_ARG;
     if (const int rc = seqs_status(*cache, seqs)) return rc;

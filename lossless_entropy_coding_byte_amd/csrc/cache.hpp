@@ -21,6 +21,8 @@ int launch_cache_write_q8(const lecb_cache_q8& c, const lecb_cache_seqs& s, cons
 int launch_cache_read_q8(const lecb_cache_q8& c, const lecb_cache_seqs& s, void* k, void* v, int type, int fill,
                          void* stream);
 
+constexpr float LOG2_E = 1.44269504088896340736f;   // the softmax is one of powers of two
+
 struct AttentionQ8 {
     lecb_cache_q8 cache;
     lecb_cache_seqs seqs;

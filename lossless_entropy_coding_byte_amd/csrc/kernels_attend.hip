@@ -225,7 +225,7 @@ int launch_attention_q8(const AttentionQ8& x, void* stream) {
     AttendArgs a = {seqs_of(x.cache, x.seqs), x.q, x.out, static_cast<const uint8_t*>(x.cache.k),
                     static_cast<const uint8_t*>(x.cache.v), x.cache.k_scale, x.cache.v_scale, x.q_token, x.q_head, x.out_token,
                     x.out_head, x.cache.heads, group, x.cache.dim, x.window < FAR ? x.window : FAR, x.causal, x.fill,
-                    x.scale * 1.44269504088896340736f, most, {}};
+                    x.scale * LOG2_E, most, {}};
     return with_float_type(x.type, [&](auto t) {
         typedef decltype(t) T;
         return with_units(x.cache.dim, [&](auto units) {

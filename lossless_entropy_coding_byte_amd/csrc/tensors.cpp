@@ -576,7 +576,8 @@ PyObject* attention_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
             scale = PyFloat_AsDouble(args[10]);
             if (scale == -1.0 && PyErr_Occurred()) throw python_error();
         }
-        if (!std::isfinite((float)scale)) refuse("attention_q8: scale is a finite number");
+        // by log2(e), as the softmax takes it
+        if (!std::isfinite((float)scale * 1.44269504f)) refuse("attention_q8: scale is a number below 2.3e38");
         const int causal = PyObject_IsTrue(args[11]);
         if (causal < 0) throw python_error();
         const int64_t window = args[12] == Py_None ? 0 : integer(args[12]);
