@@ -513,12 +513,15 @@ PyObject* cache_write_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
         if (k.size(1) != cache.c.heads || k.size(2) != cache.c.dim)
             refuse("cache_write_q8: k and v have the cache's heads and dim");
         const Sequences seqs(args + 8, cache, k.size(0), name);
-        recorded(name, k, v, cache.k_scale, cache.v_scale);   // codes and scales are constants to what follows
+        const bool grads = recorded(name, k, v, cache.k_scale, cache.v_scale);   // codes and scales are constants to what follows
         if (at::GradMode::is_enabled() && (cache.k_scale.requires_grad() || cache.v_scale.requires_grad()))
             refuse("cache_write_q8: scales that gradients are recorded for can not be written");
         for (const at::Tensor& t : {cache.k, cache.v, cache.k_scale, cache.v_scale})
             if (meets(t, k, v, seqs.table, seqs.lengths, seqs.starts)) refuse("cache_write_q8: the cache overlaps what is read");
         const Here here(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts);
+        if (grads && PyErr_WarnEx(PyExc_UserWarning, "cache_write_q8: no gradient goes back to k and v: write what is detached, or "
+                                                     "under torch.no_grad()", 1) < 0)
+            throw python_error();
         void* stream = here.stream();
         int rc;
         {
