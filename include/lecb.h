@@ -691,7 +691,7 @@ uint64_t lecb_cache_q8_bytes(uint64_t blocks, uint32_t heads, uint32_t dim, uint
  * the new tokens, or a scale that is NaN already, makes scale NaN and the block's
  * codes for this head 0.
  * Codes past a sequence's length mean nothing.  The blocks that a call writes must
- * belong to one sequence each.  Tokens whose block is not one of the cache's, or of a
+ * belong to one sequence each and stand in its row of the table once; the four arrays must not overlap.  Tokens whose block is not one of the cache's, or of a
  * sequence whose length exceeds width * block, are left out.
  * Errors: INVALID_ARG, TOO_LARGE (what the structs' comments bound). */
 int lecb_cache_write_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, const void* d_k, const void* d_v,

@@ -115,7 +115,8 @@ def cache_write_q8(cache: CacheQ8, k, v, table, lengths, starts=None) -> None:
 
     Each block has one scale for each head's keys and one for its values.  A block that holds older tokens of the
     sequence keeps its scale while that is enough; else it grows, by a quarter at least, and the older
-    codes are rounded again.  The blocks that a call writes must belong to one sequence each.  Tokens whose
+    codes are rounded again.  The blocks that a call writes must belong to one sequence each and stand in its
+    row of the table once.  Tokens whose
     block is not one of the cache's, or whose sequence is longer than its row of the table, are left out.  An
     infinity or NaN makes the block's scale for this head NaN.  No gradient goes back to k and v; where one is recorded
     for them, a warning says so."""

@@ -518,6 +518,9 @@ PyObject* cache_write_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
             refuse("cache_write_q8: scales that gradients are recorded for can not be written");
         for (const at::Tensor& t : {cache.k, cache.v, cache.k_scale, cache.v_scale})
             if (meets(t, k, v, seqs.table, seqs.lengths, seqs.starts)) refuse("cache_write_q8: the cache overlaps what is read");
+        if (meets(cache.k, cache.v, cache.k_scale, cache.v_scale) || meets(cache.v, cache.k_scale, cache.v_scale) ||
+            meets(cache.k_scale, cache.v_scale))
+            refuse("cache_write_q8: the cache's parts overlap");
         const Here here(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, seqs.table, seqs.lengths, seqs.starts);
         if (grads && PyErr_WarnEx(PyExc_UserWarning, "cache_write_q8: no gradient goes back to k and v: write what is detached, or "
                                                      "under torch.no_grad()", 1) < 0)

@@ -14,3 +14,18 @@ def test_a_scale_that_the_softmax_can_not_take(scale):
     a = tensors()
     refused("scale", lambda: lecb.attention_q8(a["q"], a["cache"], a["table"], a["lengths"], a["starts"], scale=scale))
     refused("current GPU", lambda: lecb.attention_q8(a["q"], a["cache"], a["table"], a["lengths"], a["starts"], scale=2.35e38))
+
+
+def test_a_cache_whose_parts_overlap_is_not_written():
+    """Keys' and values' workgroups would race for the same bytes; reading is another matter."""
+    ok = lecb.new_cache_q8(10, 4, 80, 64, device="cpu")
+    wide = torch.zeros(2 * ok.k.numel() + 160, dtype=torch.int8)
+    codes = lambda at: wide[at : at + ok.k.numel()].view(ok.k.shape)
+    scales = wide[2 * ok.k.numel() :].view(torch.float32)
+    for parts in ((ok.k, ok.k, ok.k_scale, ok.v_scale), (ok.k, ok.v, ok.k_scale, ok.k_scale), (codes(0), codes(64), ok.k_scale, ok.v_scale),
+                  (codes(0), codes(ok.k.numel() + 16), scales.view(10, 4), ok.v_scale), (codes(128), ok.v, ok.k_scale, wide[:160].view(torch.float32).view(10, 4))):
+        a = tensors(cache=lecb.CacheQ8(*parts, 80, 64))
+        refused("parts overlap", lambda: lecb.cache_write_q8(a["cache"], a["k"], a["v"], a["table"], a["lengths"], a["starts"]))
+        refused("current GPU", lambda: lecb.cache_read_q8(a["cache"], a["table"], a["lengths"], a["starts"], 7))
+    a = tensors(cache=lecb.CacheQ8(codes(0), codes(ok.k.numel()), scales.view(10, 4), ok.v_scale, 80, 64))   # side by side
+    refused("current GPU", lambda: lecb.cache_write_q8(a["cache"], a["k"], a["v"], a["table"], a["lengths"], a["starts"]))
