@@ -41,7 +41,14 @@ class lecb_cache_seqs(ctypes.Structure):
                 ("tokens", ctypes.c_uint32)]
 
 
+def _fits(*numbers: int) -> bool:
+    # ctypes keeps the low bits of what does not
+    return min(numbers) >= 0 and max(numbers) < 1 << 32
+
+
 def lecb_cache_q8_bytes(blocks: int, heads: int, dim: int, block: int) -> int:
+    if not _fits(blocks, heads, dim, block):
+        return 0
     return load().lecb_cache_q8_bytes(blocks, heads, dim, block)
 
 
@@ -57,6 +64,8 @@ def lecb_cache_read_q8(cache: lecb_cache_q8, seqs: lecb_cache_seqs, k, v, fill: 
 
 
 def lecb_attention_q8_workspace_bytes(cache: lecb_cache_q8, seqs: int, tokens: int, width: int, heads: int) -> int:
+    if not _fits(seqs, tokens, width, heads):
+        return 0
     return load().lecb_attention_q8_workspace_bytes(ctypes.byref(cache), seqs, tokens, width, heads)
 
 
@@ -64,6 +73,8 @@ def lecb_attention_q8(q, q_token, q_head, heads, cache: lecb_cache_q8, seqs: lec
                       out, out_token, out_head, fill: bool = True, ws=None, stream=None) -> None:
     if ws is not None and not ws.is_contiguous():
         raise ValueError("lecb_attention_q8: ws is contiguous")
+    if not _fits(heads, window):
+        raise ValueError("lecb_attention_q8: heads and window are below 2^32")
     _check(load().lecb_attention_q8(_ptr(q), q_token, q_head, _TYPES[q.dtype], heads, ctypes.byref(cache),
                                     ctypes.byref(seqs), scale, int(causal), window, _ptr(out), out_token, out_head,
                                     int(fill), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,

@@ -29,3 +29,21 @@ def test_a_cache_whose_parts_overlap_is_not_written():
         refused("current GPU", lambda: lecb.cache_read_q8(a["cache"], a["table"], a["lengths"], a["starts"], 7))
     a = tensors(cache=lecb.CacheQ8(codes(0), codes(ok.k.numel()), scales.view(10, 4), ok.v_scale, 80, 64))   # side by side
     refused("current GPU", lambda: lecb.cache_write_q8(a["cache"], a["k"], a["v"], a["table"], a["lengths"], a["starts"]))
+
+
+def test_numbers_past_32_bits():
+    """Not taken for what their low bits say."""
+    wrap = 1 << 32
+    for bad in ((10 + wrap, 4, 80, 64), (10, 4 + wrap, 80, 64), (10, 4, 80 + wrap, 64), (10, 4, 80, 64 + wrap), (10 + (1 << 64), 4, 80, 64)):
+        assert lecb.lecb_cache_q8_bytes(*bad) == 0
+        refused("new_cache_q8", lambda: lecb.new_cache_q8(*bad, device="cpu"))
+    ok = lecb.new_cache_q8(10, 4, 80, 64, device="cpu")
+    refused("CacheQ8", lambda: lecb.CacheQ8(ok.k, ok.v, ok.k_scale, ok.v_scale, 80, 64 + wrap))
+    cache, seqs = structs()
+    args = dict(seqs=3, tokens=7, width=1000, heads=8)
+    assert lecb.lecb_attention_q8_workspace_bytes(cache, **args) > 0
+    for name in args:
+        assert lecb.lecb_attention_q8_workspace_bytes(cache, **{**args, name: args[name] + wrap}) == 0
+    q = torch.zeros(7, 8, 80)
+    for heads, window in ((8 + wrap, 0), (8, 5 + wrap), (8, -1)):
+        refused("below 2.32", lambda: lecb.lecb_attention_q8(q, 640, 80, heads, cache, seqs, 0.1, True, window, q, 640, 80))
