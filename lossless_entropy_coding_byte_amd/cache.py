@@ -144,7 +144,7 @@ def cache_read_q8(cache: CacheQ8, table, lengths, starts=None, tokens: int | Non
     if tokens is None:
         if starts is not None:
             raise ValueError("cache_read_q8: with starts the number of rows, tokens, is needed")
-        tokens = lengths.shape[0]
+        tokens = lengths.numel()
     return _tensors.cache_read_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.dim, cache.block, table, lengths,
                                   starts, tokens, dtype)
 

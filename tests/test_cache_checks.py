@@ -47,3 +47,8 @@ def test_numbers_past_32_bits():
     q = torch.zeros(7, 8, 80)
     for heads, window in ((8 + wrap, 0), (8, 5 + wrap), (8, -1)):
         refused("below 2.32", lambda: lecb.lecb_attention_q8(q, 640, 80, heads, cache, seqs, 0.1, True, window, q, 640, 80))
+
+
+def test_lengths_without_a_dimension():
+    a = tensors()
+    refused("lengths", lambda: lecb.cache_read_q8(a["cache"], a["table"], torch.zeros((), dtype=torch.int32)))
