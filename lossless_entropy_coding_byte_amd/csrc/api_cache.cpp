@@ -31,6 +31,11 @@ int seqs_status(const lecb_cache_q8& c, const lecb_cache_seqs* s) {
         return LECB_ERR_INVALID_ARG;
     return aligned(s->starts, 4) ? LECB_OK : LECB_ERR_INVALID_ARG;
 }
+// Each workgroup of the attention, one to 16 rows of a sequence and head, looks through all sequences for its own: 52 ms
+// at 2^29 (8192 sequences of a row, 32 heads to 8, with starts), four times that with twice the sequences.
+bool search_ok(uint64_t seqs, uint64_t tokens, uint64_t heads, uint64_t cache_heads) {
+    return seqs * (seqs * cache_heads + tokens * heads / 16) < (1ull << 35);
+}
 bool tensor_ok(const void* p, int type) { return p && aligned(p, elem_bytes(type)); }
 
 }  // namespace
@@ -65,7 +70,8 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
 uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t seqs, uint32_t tokens, uint32_t width,
                                            uint32_t heads) {
     if (!cache || !geometry_ok(*cache) || heads < 1 || heads % cache->heads || seqs >= (1u << 20) ||
-        tokens >= (1u << 27) || (uint64_t)width * cache->block >= (1ull << 30) || !seqs || !tokens)
+        tokens >= (1u << 27) || (uint64_t)width * cache->block >= (1ull << 30) || !seqs || !tokens ||
+        !search_ok(seqs, tokens, heads, cache->heads))
         return 0;
     return attention_q8_workspace(*cache, seqs, tokens, width, heads);
 }
@@ -79,7 +85,8 @@ int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_
         return LECB_ERR_INVALID_ARG;
     if (const int rc = seqs_status(*cache, seqs)) return rc;
     if (seqs->tokens == 0) return LECB_OK;
-    if ((uint64_t)seqs->tokens * heads >= (1ull << 27) || (uint64_t)seqs->seqs * cache->heads >= (1ull << 22))
+    if ((uint64_t)seqs->tokens * heads >= (1ull << 27) || (uint64_t)seqs->seqs * cache->heads >= (1ull << 22) ||
+        !search_ok(seqs->seqs, seqs->tokens, heads, cache->heads))
         return LECB_ERR_TOO_LARGE;
     if (seqs->seqs == 0 || !tensor_ok(d_q, type) || !tensor_ok(d_out, type) || out_head_stride < cache->dim ||
         out_token_stride < cache->dim)

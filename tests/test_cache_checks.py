@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import lossless_entropy_coding_byte_amd as lecb
-from test_cache_host import INVALID, call_attend, refused, structs, tensors
+from test_cache_host import INVALID, TOO_LARGE, call_attend, refused, structs, tensors
 
 
 @pytest.mark.parametrize("scale", [2.36e38, 3.4e38, -2.36e38])
@@ -52,3 +52,16 @@ def test_numbers_past_32_bits():
 def test_lengths_without_a_dimension():
     a = tensors()
     refused("lengths", lambda: lecb.cache_read_q8(a["cache"], a["table"], torch.zeros((), dtype=torch.int32)))
+
+
+def test_more_sequences_than_a_search_bears():
+    """Each workgroup looks through all sequences: calls that would take minutes of that are refused."""
+    many = dict(seqs=1 << 17, tokens=1 << 17)
+    assert call_attend(*structs(**many)) == TOO_LARGE
+    cache, _ = structs()
+    size = lambda seqs, tokens: lecb.lecb_attention_q8_workspace_bytes(cache, seqs, tokens, 1000, 8)
+    assert size(1 << 17, 1 << 17) == 0 and size(1 << 13, 1 << 23) == 0
+    assert size(1 << 16, 1 << 16) > 0 and size(1 << 12, 1 << 23) > 0 and size(1 << 10, (1 << 24) - 1) > 0
+    a = tensors(q=torch.zeros(1, 8, 80).expand(1 << 17, 8, 80), table=torch.zeros(1 << 17, 1, dtype=torch.int32),
+                lengths=torch.zeros(1 << 17, dtype=torch.int32))
+    refused("below 2.35", lambda: lecb.attention_q8(a["q"], a["cache"], a["table"], a["lengths"]))
