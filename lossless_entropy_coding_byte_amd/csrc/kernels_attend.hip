@@ -213,7 +213,9 @@ uint64_t attention_q8_workspace(const lecb_cache_q8& c, uint64_t seqs, uint64_t 
         return bytes_of(shape_of(rows, c.dim, c.heads, group, c.block, seqs, tokens, width, few_most(LECB_F32, c.dim, tokens * group, seqs)),
                         rows, c.dim);
     };
-    const uint64_t many = bytes(128), more = bytes(256);
+    // the form for many, where a sequence that had all rows would go by it in any type
+    const bool any = tokens * group > few_most(LECB_BF16, c.dim, tokens * group, seqs);
+    const uint64_t many = any ? bytes(128) : 0, more = any ? bytes(256) : 0;
     return bytes(FEW_ROWS) + (many > more ? many : more);
 }
 

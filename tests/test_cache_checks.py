@@ -65,3 +65,14 @@ def test_more_sequences_than_a_search_bears():
     a = tensors(q=torch.zeros(1, 8, 80).expand(1 << 17, 8, 80), table=torch.zeros(1 << 17, 1, dtype=torch.int32),
                 lengths=torch.zeros(1 << 17, dtype=torch.int32))
     refused("below 2.35", lambda: lecb.attention_q8(a["q"], a["cache"], a["table"], a["lengths"]))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_the_workspace_of_a_decoding_step(dim):
+    """Calls that never go by the form for many rows have room for the other's sums alone: 2048 parts of 16 rows."""
+    cache, _ = structs(heads=8, dim=dim, blocks=1 << 20)
+    few = 2048 * 16 * (dim + 4) * 4
+    for seqs, tokens, heads in ((64, 64, 32), (1, 1, 64), (1, 16, 32), (16, 64, 32)):
+        assert 0 < lecb.lecb_attention_q8_workspace_bytes(cache, seqs, tokens, 4096, heads) <= few
+    for seqs, tokens, heads in ((64, 65, 32), (1, 17, 32)):
+        assert lecb.lecb_attention_q8_workspace_bytes(cache, seqs, tokens, 4096, heads) > few
