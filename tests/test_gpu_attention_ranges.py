@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import lossless_entropy_coding_byte_amd as lecb
-from cache_helpers import BF16, F16, F32, attention, random_cache, starts_of, tables
+from cache_helpers import BF16, F16, F32, attention, places, random_cache, starts_of, tables
 from test_gpu_attention import near, queries
 from test_gpu_layers import DEV, gen
 
@@ -148,3 +148,38 @@ def test_queries_and_keys_of_opposite_size(size, news, dtype):
             cache.k_scale.mul_(2.0**30 if size > 1 else 1.0)
         want, tol = attention(q, cache, table, lens, starts, scale=scale)
         near(lecb.attention_q8(q, cache, table, lens, starts, scale=scale), want, tol)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news", [12, 300])
+def test_rows_of_one_call_that_see_different_blocks(news, dtype):
+    """A block that some rows of a call see and others do not, bad in each way: the others' results are the formula's, those
+    of rows before it the same bits.  Codes behind the end are left over from other tokens."""
+    g = gen(19)
+    cache = random_cache(g, 14, 2, 80, 32, DEV)
+    for first in (384, (390 - news // 2) // 32 * 32):      # the last block, and one in the middle of the rows
+        table, lens = tables(g, [390], 32, 14, DEV)
+        at, starts = first // 32, starts_of([news], DEV)
+        q = queries(g, news, 4, 80, dtype)
+        page, kept = table[0, at].item(), [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale, table)]
+        want, tol = attention(q, cache, table, lens, starts, window=40)
+        plain = lecb.attention_q8(q, cache, table, lens, starts, window=40)
+        pos = torch.arange(390 - news, 390)
+        before, past = pos < first, pos - 39 > first + 31
+        for change in (lambda: cache.k_scale[page].fill_(float("inf")), lambda: cache.k_scale[page].fill_(float("nan")),
+                       lambda: cache.v_scale[page].fill_(-float("inf")), lambda: cache.v_scale[page].fill_(float("nan")),
+                       lambda: cache.v_scale[page].fill_(3e38), lambda: cache.v_scale[page].fill_(2.0**-149),
+                       lambda: cache.k[page].fill_(-128), lambda: cache.v[page].fill_(-128),
+                       lambda: table[0, at].fill_(-1), lambda: table[0, at].fill_(14), lambda: table[0, at].fill_(1 << 30)):
+            change()
+            got = lecb.attention_q8(q, cache, table, lens, starts, window=40)
+            assert torch.equal(got[before.to(DEV)], plain[before.to(DEV)])
+            near(got[past.to(DEV)], want[past], tol[past])
+            for t, was in zip((cache.k, cache.v, cache.k_scale, cache.v_scale, table), kept):
+                t.copy_(was)
+        # codes behind the sequence's end
+        for c, keys in ((cache.k, True), (cache.v, False)):
+            c[table[0, 12].item()][:, places(32, 80, keys)[390 - 384 :].reshape(-1)] = -128
+        assert torch.equal(lecb.attention_q8(q, cache, table, lens, starts, window=40), plain)
+        for t, was in zip((cache.k, cache.v), kept):
+            t.copy_(was)
