@@ -718,7 +718,8 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  * token stride + head * head stride + i; out must not overlap q.
  * Codes are exact in the products, q to 2^-29 of its row's largest element (F16:
  * exact), sums and the softmax have 32 bits; its weights enter the second product
- * with 11 bits (BF16 out) or 22, down to 2^-36 of the largest of weight times scale.
+ * with 22 bits, down to 2^-36 of the largest of weight times scale.  BF16 sequences of more than 64 rows (tokens *
+ * heads / cache heads) may go with 11: an eighth of what the results' own rounding is off by.
  * Values whose scales are below 2^-60 lose as many of these 36 bits as they are below it.
  * A row with an infinity or NaN in q is NaN, and so is one that sees a block
  * with a scale that is not finite, a block that is not one of the

@@ -32,7 +32,8 @@ struct FewMemory {
 
 template <typename T, int U, int WAVES>
 __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t h, FewMemory<T, U, WAVES>& mem) {
-    constexpr int ROWS = FEW_ROWS, NQ = Parts<T>::Q, NP = Parts<T>::P, THREADS = 64 * WAVES;
+    // weights in two parts, 22 bits, for every type: the second products are not what bounds this form
+    constexpr int ROWS = FEW_ROWS, NQ = Parts<T>::Q, NP = 2, THREADS = 64 * WAVES;
     const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     Work k;
     if (!work_of<ROWS>(a, it, h, k)) return;
@@ -146,7 +147,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
         for (int i = 0; i < 8; ++i) {
             v[i] = exp2_of(fmaf(v[i], f, base));
             sum += v[i];
-            v[i] = NP > 1 ? product(v[i], down) : v[i] * down;
+            v[i] = product(v[i], down);
         }
 #pragma unroll
         for (int j = 0; j < NP; ++j)

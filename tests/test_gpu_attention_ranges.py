@@ -183,3 +183,19 @@ def test_rows_of_one_call_that_see_different_blocks(news, dtype):
         assert torch.equal(lecb.attention_q8(q, cache, table, lens, starts, window=40), plain)
         for t, was in zip((cache.k, cache.v), kept):
             t.copy_(was)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_results_of_16_bits_are_those_of_32_rounded(dim, dtype):
+    """Few rows: errors before the last rounding are those that 32 bits' results may have, so a result lies between the
+    roundings of the ends of that interval.  Few tokens, of like weights: what a weight is off by shows."""
+    g = gen(dim + 1)
+    lengths = [2 + s % 8 for s in range(60)]
+    cache = random_cache(g, 60, 2, dim, 32, DEV)
+    table, lens = tables(g, lengths, 32, 60, DEV)
+    q = queries(g, 60, 8, dim, dtype, size=0.1)
+    want, tol = attention(q.float(), cache, table, lens)
+    got = lecb.attention_q8(q, cache, table, lens).cpu()
+    low, high = ((want + s * tol).to(dtype) for s in (-1, 1))
+    assert bool(((low <= got) & (got <= high)).all())
