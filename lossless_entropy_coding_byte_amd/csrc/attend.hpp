@@ -294,6 +294,8 @@ __device__ inline float max_of_quarters(float v) {
     return max_of_halves(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
 }
 __device__ inline float inf() { return __uint_as_float(0x7f800000u); }
+// Whether s is neither infinite nor NaN, in scalar registers where s is (attend_few has none of the others to spare).
+__device__ inline bool finite(float s) { return __float_as_uint(s) << 1 < 0xff000000u; }
 
 // A block's scale of keys; NaN where it is no number or there is no such block: an infinite one would leave tokens
 // whose products are negative out of the softmax, which their keys, infinities and 0 times infinity, are not.

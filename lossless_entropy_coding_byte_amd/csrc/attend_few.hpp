@@ -114,7 +114,7 @@ __device__ inline void attend_few(const AttendArgs& a, const Item& it, uint32_t 
 
         // all rows see all of the tile's tokens, and the larger product is the larger score
         const bool plain = at >= lo_most && at + (int)TILE_TOKENS - 1 <= hi_least && a.scale >= 0.0f && ks >= 0.0f;
-        const bool number = fabsf(vs) < inf();
+        const bool number = finite(vs);
         const float down = number ? vs * P_DOWN : 0.0f, unit = scale_exponent(vs);
         float f = factor.times(ks), v[8], most = -inf();
 #pragma unroll

@@ -16,9 +16,10 @@ template <typename T, int U>
 constexpr bool HAS_MANY = sizeof(T) == 2 || U < 6;
 
 // A workgroup takes one item.  Those of the first launch without one see to the
-// rows of no sequence.
+// rows of no sequence.  16-bit rows of 128 dimensions are held to four workgroups a compute unit: with three, each
+// finds its item while fewer others load (1024 sequences of 512 tokens 376 us, with four 334; one of 32768 with 64 rows 50 and 48).
 template <typename T, int U>
-__global__ __launch_bounds__(THREADS, U * sizeof(T) <= 16 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(THREADS, U * sizeof(T) <= 8 ? 4 : U * sizeof(T) <= 16 ? 2 : 1) void attend_few_kernel(AttendArgs a) {
     __shared__ __attribute__((aligned(16))) FewMemory<T, U, WAVES> memory;
     const uint32_t h = blockIdx.x % a.heads, w = blockIdx.x / a.heads;
     Item it;
