@@ -730,9 +730,9 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  * d_ws: lecb_attention_q8_workspace_bytes (may be 0, then NULL is taken); its
  * contents do not matter before or after.
  * heads is a multiple of the cache's.  Errors: INVALID_ARG (window >= 2^31 too), WORKSPACE,
- * TOO_LARGE (also tokens * heads >= 2^27, seqs * cache heads >= 2^22, and seqs * (seqs * cache heads + tokens *
- * heads / 16) >= 2^35: every workgroup looks through all sequences, and a call near that bound takes seconds.  8192
- * sequences of 512 tokens, a row each, 32 heads to 8: 52 ms with starts, 8 without). */
+ * TOO_LARGE (also tokens * heads >= 2^27, seqs * cache heads >= 2^22, and seqs * (5 * seqs * cache heads + tokens *
+ * heads / 128) >= 2^37, / 16 for F32 of more than 128 dimensions: every workgroup looks through all sequences, and a
+ * call near that bound takes seconds.  8192 sequences of 512 tokens, a row each, 32 heads to 8: 52 ms with starts, 8 without). */
 uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t seqs, uint32_t tokens,
                                            uint32_t width, uint32_t heads);
 int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_stride, int type, uint32_t heads,

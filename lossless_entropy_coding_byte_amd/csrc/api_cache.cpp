@@ -31,11 +31,13 @@ int seqs_status(const lecb_cache_q8& c, const lecb_cache_seqs* s) {
         return LECB_ERR_INVALID_ARG;
     return aligned(s->starts, 4) ? LECB_OK : LECB_ERR_INVALID_ARG;
 }
-// Each workgroup of the attention, one to 16 rows of a sequence and head, looks through all sequences for its own: 52 ms
-// at 2^29 (8192 sequences of a row, 32 heads to 8, with starts), four times that with twice the sequences.
-bool search_ok(uint64_t seqs, uint64_t tokens, uint64_t heads, uint64_t cache_heads) {
-    return seqs * (seqs * cache_heads + tokens * heads / 16) < (1ull << 35);
+// Each workgroup of the attention looks through all sequences for its own rows: 52 ms for 8192 sequences of a row, 32
+// heads to 8, with starts (2^31.3 here), four times that with twice the sequences.  A sequence and head has up to four
+// workgroups of 16 rows or one to 128.
+bool search_ok(uint64_t seqs, uint64_t tokens, uint64_t heads, uint64_t cache_heads, uint64_t rows) {
+    return seqs * (5 * seqs * cache_heads + tokens * heads / rows) < (1ull << 37);
 }
+uint64_t rows_of(int type, uint32_t dim) { return type == LECB_F32 && dim > 128 ? 16 : 128; }   // of a workgroup, of many
 bool tensor_ok(const void* p, int type) { return p && aligned(p, elem_bytes(type)); }
 
 }  // namespace
@@ -71,7 +73,7 @@ uint64_t lecb_attention_q8_workspace_bytes(const lecb_cache_q8* cache, uint32_t 
                                            uint32_t heads) {
     if (!cache || !geometry_ok(*cache) || heads < 1 || heads % cache->heads || seqs >= (1u << 20) ||
         tokens >= (1u << 27) || (uint64_t)width * cache->block >= (1ull << 30) || !seqs || !tokens ||
-        !search_ok(seqs, tokens, heads, cache->heads))
+        !search_ok(seqs, tokens, heads, cache->heads, 128))
         return 0;
     return attention_q8_workspace(*cache, seqs, tokens, width, heads);
 }
@@ -86,7 +88,7 @@ int lecb_attention_q8(const void* d_q, uint64_t q_token_stride, uint64_t q_head_
     if (const int rc = seqs_status(*cache, seqs)) return rc;
     if (seqs->tokens == 0) return LECB_OK;
     if ((uint64_t)seqs->tokens * heads >= (1ull << 27) || (uint64_t)seqs->seqs * cache->heads >= (1ull << 22) ||
-        !search_ok(seqs->seqs, seqs->tokens, heads, cache->heads))
+        !search_ok(seqs->seqs, seqs->tokens, heads, cache->heads, rows_of(type, cache->dim)))
         return LECB_ERR_TOO_LARGE;
     if (seqs->seqs == 0 || !tensor_ok(d_q, type) || !tensor_ok(d_out, type) || out_head_stride < cache->dim ||
         out_token_stride < cache->dim)

@@ -591,9 +591,9 @@ PyObject* attention_q8(PyObject*, PyObject* const* args, Py_ssize_t count) {
             refuse("attention_q8: window is 1 to 2^31 - 1 tokens and goes with causal attention");
         if (tokens * heads >= 1 << 27 || (int64_t)seqs.s.seqs * cache.c.heads >= 1 << 22)
             refuse("attention_q8: fewer than 2^27 rows by heads, and 2^22 sequences by the cache's heads");
-        const int64_t all = seqs.s.seqs;
-        if (all * (all * cache.c.heads + tokens * heads / 16) >= int64_t(1) << 35)
-            refuse("attention_q8: sequences by (sequences by the cache's heads, and a 16th of rows by heads) below 2^35");
+        const int64_t all = seqs.s.seqs, rows = t == at::kFloat && cache.c.dim > 128 ? 16 : 128;
+        if (all * (5 * all * cache.c.heads + tokens * heads / rows) >= int64_t(1) << 37)
+            refuse("attention_q8: sequences by (5 sequences by the cache's heads, and a 128th of rows by heads) below 2^37");
         at::Tensor out = optional(args[13], "attention_q8: out"), ws = optional(args[14], "attention_q8: ws");
         const bool given = out.defined();
         const bool grads = recorded(name, q, cache.k_scale, cache.v_scale, out);
