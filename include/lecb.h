@@ -688,8 +688,8 @@ uint64_t lecb_cache_q8_bytes(uint64_t blocks, uint32_t heads, uint32_t dim, uint
  *   A block without older tokens gets scale = need.
  * q = x / scale rounded to nearest (the exact quotient decides, half a step goes
  * to the even code) in -127..127; 0 where scale is 0.  An infinity or NaN among
- * the new tokens, or a scale that is NaN already, makes scale NaN and the block's
- * codes for this head 0.
+ * the new tokens makes scale NaN and the block's codes for this head 0; a scale that is
+ * NaN already stays so, and the new tokens' codes are 0.
  * Codes past a sequence's length mean nothing.  The blocks that a call writes must
  * belong to one sequence each and stand in its row of the table once; the four arrays must not overlap.  Tokens whose block is not one of the cache's, or of a
  * sequence whose length exceeds width * block, are left out.
@@ -715,7 +715,7 @@ int lecb_cache_read_q8(const lecb_cache_q8* cache, const lecb_cache_seqs* seqs, 
  * up to the row's own (causal = 1) or all of them (causal = 0); with a window
  * (> 0, causal = 1 only) over the last `window` of these.  scale * log2(e) is finite.  A row that sees
  * nothing is 0.  q and out: type F32, BF16 or F16, element (row, head, i) at row *
- * token stride + head * head stride + i; out must not overlap q.
+ * token stride + head * head stride + i; out must not overlap q, nor its rows or heads each other.
  * Codes are exact in the products, q to 2^-29 of its row's largest element (F16:
  * exact), sums and the softmax have 32 bits; its weights enter the second product
  * with 22 bits, down to 2^-36 of the largest of weight times scale.  BF16 sequences of more than 64 rows (tokens *

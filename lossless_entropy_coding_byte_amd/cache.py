@@ -159,9 +159,8 @@ def attention_q8(q, cache: CacheQ8, table, lengths, starts=None, scale: float | 
     no sequence, which a given ``out`` keeps as it was.  A row that sees a block with a scale that is not finite, one
     that is not the cache's, or that belongs to a sequence longer than its row of the table, is NaN; what
     is masked never matters.  The order of sums follows from the lengths of all sequences.  Products and sums have 32
-    bits, the softmax's weights 22 in the second product; 11 for bfloat16 where a sequence has more than 64 rows by heads of
-    one cache head.  out: must not
-    overlap what is read.  ws: a uint8 workspace of lecb_attention_q8_workspace_bytes that the caller keeps; calls
-    that overlap in time must not share one."""
+    bits, the softmax's weights 22 in the second product; 11 for bfloat16 where a sequence has more than 64 rows by
+    heads of one cache head.  out: must not overlap what is read.  ws: a uint8 workspace of
+    lecb_attention_q8_workspace_bytes that the caller keeps; calls that overlap in time must not share one."""
     return _tensors.attention_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.dim, cache.block, q, table, lengths,
                                  starts, scale, causal, window, out, ws)

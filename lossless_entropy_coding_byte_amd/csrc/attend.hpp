@@ -256,12 +256,15 @@ struct Parts<float> {
 
 // The running state of a row's softmax, in units that make it last: weights are
 // p = 2^(x + ref), x the score times log2(e), and ref = 30 - max(x + e) where
-// 2^e is the power of two just above the scale of x's values (e >= -60).  So p
-// times that scale, what the second product takes, is at most 2^30 whatever the
-// scales are, with 36 bits below it before halves run out, and p itself stays
-// within 2^90 and 2^-94.  ref follows a larger maximum only once it is LAG behind,
-// as sums have to be scaled whenever it moves: in a prompt of 4096 tokens after
-// nearly each pair of tiles without that, once or twice with it.
+// 2^e is the power of two just above the scale of x's values, -60 <= e <= 128.  ref
+// follows a larger maximum only once it is LAG behind, as sums have to be scaled
+// whenever it moves: in a prompt of 4096 tokens after nearly each pair of tiles
+// without that, once or twice with it.  So p times that scale, what the second
+// product takes, is at most 2^34, with 36 bits below a largest of 2^30 before halves
+// run out; scales below 2^-60 lose as many of these as they are below it.  p itself is
+// at most 2^94, and the one that ref was taken from 2^-98 or more: beside the largest
+// scale there can be, the sum of weights has 28 bits left in the exponential's range
+// below that one, and one more for each bit that the scale is smaller.
 constexpr float REF_TOP = 30.0f, LAG = 4.0f;
 constexpr float P_DOWN = 0x1p-19f;   // into halves: at most 2^(30 + LAG - 19)
 constexpr float P_DOWN_LOG2 = -19.0f;

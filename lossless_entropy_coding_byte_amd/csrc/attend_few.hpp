@@ -14,13 +14,13 @@ namespace lecb {
 // product's operand as they are; values are stored in that order of tokens.
 // Neither codes nor scores go through LDS.
 //
-// Bound by HBM, with vector instructions (codes to halves, 1.25 a code) at two
-// fifths of their rate: 64 sequences of up to 8192 tokens, 32 heads to 8 of 128
+// Bound by HBM, with vector instructions (codes to halves, 1.25 a code) at half
+// of their rate: 64 sequences of up to 8192 tokens, 32 heads to 8 of 128
 // dimensions, 96 us, 5.6 TB/s of codes; one token after 262144 88 us, 6.1 TB/s.  With two sets of
 // registers for codes (a whole tile ahead, 3 waves a SIMD instead of 4) these took 104
 // and 92.  Eight waves a workgroup: 104 -> 111 and 95 -> 93 with all launches.  A call
-// of few tokens lasts as long as its chain of loads (lengths, blocks, codes): 6.5 us
-// for 1000 tokens and 2.6 of attend_join_kernel's.
+// of few tokens lasts as long as its chain of loads (lengths, blocks, codes): 6.7 us
+// for 1000 tokens and 2.7 of attend_join_kernel's.
 template <typename T, int U, int WAVES>
 struct FewMemory {
     union {

@@ -18,8 +18,9 @@ namespace lecb {
 // Bound by instruction issue: of a tile and 32 rows, 512 cycles of products stand
 // beside some 600 of vector instructions, a third of them exponentials and a
 // fifth (a tenth with eight waves) codes to halves.  512 tokens after 32256, 32 heads to 8 of 128
-// dimensions: 298 us, 915 TFLOP/s, the matrix units busy 42 % of the time (four waves
-// and two workgroups a compute unit 323); two prompts of up to 4096 tokens 265, 690.  Dimensions of 96
+// dimensions: 300 us, 910 TFLOP/s, the matrix units busy 42 % of the time (four waves
+// and two workgroups a compute unit 323), 460 in fp16 and 710 in fp32 with their weights' and queries' parts;
+// two prompts of up to 4096 tokens 276 with the other launches, 660.  Dimensions of 96
 // have three units, which eight waves do not share evenly; more than 128, or 32 bits, need
 // the registers of two waves.  Tried and slower: 64 rows a wave (half the reads of LDS, but one
 // wave a SIMD, and sums outside of the vector registers: 340 -> 399 us), all products of a step

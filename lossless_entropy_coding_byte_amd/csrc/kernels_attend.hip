@@ -153,10 +153,11 @@ uint64_t bytes_of(const Shape& s, uint64_t rows, uint32_t dim) {
 }
 
 // Rows of a sequence up to which the form for few takes it.  Both forms, us, heads
-// of 128 dimensions in bf16: 16 sequences of 8192 tokens with 64 rows each 124 and 149,
-// one of 32768 48 and 52, 16 of 1024 33 and 39; with 128 rows 65 and 55 (32768), 34
-// and 43 (1024), with 512 181 and 98, 98 and 65; dimensions of 64 and 256 and 32 bits cross
-// between 64 and 256 rows too.  Each form takes a launch, 4 to 5 us where it finds nothing to
+// of 128 dimensions in bf16: 16 sequences of 8192 tokens with 64 rows each 131 and 156,
+// one of 32768 48 and 52, 16 of 1024 34 and 36; with 128 rows 206 and 162 (8192), 66 and 55
+// (32768), 35 and 41 (1024), with 512 655 and 317, 186 and 96, 104 and 62; dimensions of 64 and 256 and
+// 32 bits cross between 64 and 256 rows too.  Neither the heads of the cache nor the lengths enter: with
+// one head or short sequences the form for many leaves compute units idle that the other would use.  Each form takes a launch, 4 to 5 us where it finds nothing to
 // do: a call of few rows in all goes by the form for few alone, one sequence by one of them.
 uint32_t few_most(int type, uint32_t dim, uint64_t rows, uint64_t seqs) {
     if ((type == LECB_F32 && dim > 128) || rows <= (seqs > 1 ? 256 : 64)) return 0x7fffffffu;
